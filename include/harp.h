@@ -482,6 +482,109 @@ harp_status harp_linear_fused_noalloc(const harp_rotation *V, const harp_qweight
                                       int32_t M, harp_stream stream);
 
 /*
+ * 8-bit floating point (e4m3: 4 exponent and 3 mantissa bits, largest value
+ * 448, no infinities, codes 0x7f and 0xff NaN) next to the low-bit linears:
+ * for layers kept at 8 bits, for experts, and for the norm and the gated
+ * activation in front of them.
+ *
+ * Rows of codes.  Each run of 128 consecutive values v of a row (the last
+ * run may be shorter) has one float32 scale s = max(max|v| / 448, 2^-126)
+ * and the codes c = e4m3(v / s), nearest even; c s is the value held.  v is
+ * float32 and not rounded before; v / s is formed as v (1 / s).  A NaN stays
+ * a NaN in its place and does not enter the maximum; a run that holds an
+ * infinity has an infinite scale, so every value of it reads as NaN.
+ *   q        [M][D] codes, one byte each
+ *   q_scale  [M][ceil(D/128)] float32
+ *
+ * Weights.  One scale per 128 x 128 block of each matrix (blocks at the
+ * right and lower edge may be smaller):
+ *   w      [experts][N][K] codes;  K a multiple of 16, 16 <= K <= HARP_MAX_DIM
+ *   scale  [experts][ceil(N/128)][ceil(K/128)] float32
+ *   experts  1 for harp_fp8_gemm, 1 .. HARP_MAX_EXPERTS for the grouped form
+ */
+#define HARP_MAX_EXPERTS 1024
+#define HARP_MAX_NORM_DIM 32768
+typedef struct harp_fp8_weight {
+  int32_t N;
+  int32_t K;
+  int32_t experts;
+  const uint8_t *w;
+  const float *scale;
+} harp_fp8_weight;
+
+/*
+ * Residual addition and root-mean-square norm of M rows, the step in front
+ * of every linear (harp_rotate_in / harp_linear_fused take y, the FP8
+ * products the codes of harp_rmsnorm_fp8):
+ *     h = x + r,   r' = h rounded to x_dt,   y = h / sqrt(mean(h^2) + eps) * w.
+ * The norm is taken of h in float32, before r' is rounded; the sum of
+ * squares is float32.
+ *   x             [M][D] of x_dt;  weight [D] of w_dt
+ *   residual      [M][D] of x_dt, or NULL (h = x)
+ *   residual_out  [M][D] of x_dt, or NULL (r' is not stored; must be NULL
+ *                 when residual is); may be residual itself (in place), any
+ *                 other overlap is not allowed
+ *   eps           finite, >= 0 (0 makes a row of zeros NaN)
+ *   y             [M][D] of y_dt (bf16: nearest even);  1 <= D <=
+ *                 HARP_MAX_NORM_DIM
+ *   q, q_scale    codes of y as above;  D a multiple of 16
+ */
+harp_status harp_rmsnorm(const void *x, harp_dtype x_dt, const void *residual,
+                         void *residual_out, const void *weight, harp_dtype w_dt, float eps,
+                         void *y, harp_dtype y_dt, int32_t M, int32_t D, harp_stream stream);
+harp_status harp_rmsnorm_fp8(const void *x, harp_dtype x_dt, const void *residual,
+                             void *residual_out, const void *weight, harp_dtype w_dt, float eps,
+                             uint8_t *q, float *q_scale, int32_t M, int32_t D,
+                             harp_stream stream);
+
+/*
+ * The gated activation between an MLP's (or an expert's) two products, as
+ * codes: v = g / (1 + exp(-g)) * u in float32.
+ *   gate_up     [M][2 D] of x_dt, a row's D gates g first, then its D values u
+ *   q, q_scale  codes of v as above;  D a multiple of 16, 16 <= D <=
+ *               HARP_MAX_DIM
+ */
+harp_status harp_silu_mul_fp8(const void *gate_up, harp_dtype x_dt, uint8_t *q, float *q_scale,
+                              int32_t M, int32_t D, harp_stream stream);
+
+/*
+ * y[m][n] = sum_b a_scale[m][b] W->scale[n / 128][b] sum_{k in run b} a[m][k] w[n][k]
+ * on the matrix cores: each run of 128 inputs is summed there, its two
+ * scales are multiplied in float32 (their product must not overflow), and
+ * the scaled runs are added in float32.  Any M.  For a bf16 y the run's sum
+ * is the FP8 matrix instruction's, which keeps the products of each eight
+ * consecutive inputs to 2^-13 of the largest of them; for a float32 y it is
+ * a float32 sum of the exact products (the codes taken to bf16, half the
+ * matrix rate).
+ *   a        [M][W->K] codes;  a_scale [M][ceil(K/128)] float32
+ *   y        [M][W->N] of y_dt (bf16: nearest even)
+ */
+harp_status harp_fp8_gemm(const harp_fp8_weight *W, const uint8_t *a, const float *a_scale,
+                          void *y, harp_dtype y_dt, int32_t M, harp_stream stream);
+
+/*
+ * The same product for M rows that are sorted by expert, with as many rows
+ * for each as a router chose: for offsets[e] <= i < offsets[e + 1]
+ *     y[i] = W_e a[rows[i]].
+ *   a        [a_rows][W->K] codes;  a_scale [a_rows][ceil(K/128)] float32
+ *   rows     [M] int32, or NULL for rows[i] = i (then a_rows >= M).  The same
+ *            row may occur any number of times.  An entry outside
+ *            [0, a_rows) makes its output row zero.
+ *   offsets  [experts + 1] int32, not decreasing, within [0, M] (values
+ *            outside are taken as the nearer end, and an expert whose end
+ *            lies before its start has no rows).  offsets that
+ *            decrease leave y undefined, but nothing outside y is written.
+ *   y        [M][W->N] of y_dt.  Rows before offsets[0] and from
+ *            offsets[experts] on are left as they were.
+ * rows and offsets are device memory and read on the stream: nothing waits
+ * for the host, and one captured graph serves any routing of M rows.
+ */
+harp_status harp_fp8_gemm_grouped(const harp_fp8_weight *W, const uint8_t *a,
+                                  const float *a_scale, int32_t a_rows, const int32_t *rows,
+                                  const int32_t *offsets, void *y, harp_dtype y_dt, int32_t M,
+                                  harp_stream stream);
+
+/*
  * Test hook, not on the hot path: writes the dense w_hat [N][K] as float32
  * (exact) or bf16 (nearest even), through the same device unpack and
  * dequant code the products use (the stand-in per-group uniform grid

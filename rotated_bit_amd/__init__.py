@@ -5,7 +5,8 @@ The Python surface is the ctypes binding in _lib (argument marshalling only);
 importing this package fails if libharp.so has not been built.
 """
 from ._lib import (  # noqa: F401
-    HARP_BF16, HARP_F32, HarpError, MixedRotation, QWeight, Rotation, harp_dequant,
+    HARP_BF16, HARP_F32, FP8Weight, HarpError, MixedRotation, harp_fp8_gemm,
+    harp_fp8_gemm_grouped, harp_rmsnorm, harp_rmsnorm_fp8, harp_silu_mul_fp8, QWeight, Rotation, harp_dequant,
     harp_deq_gemm, harp_deq_gemm_workspace_bytes, harp_deq_gemv, harp_deq_gemv_ws,
     harp_deq_gemv_workspace_bytes, harp_last_hip_error, harp_linear_fused,
     harp_linear_fused_noalloc, harp_linear_chain, harp_linear_chain_workspace_bytes,

@@ -40,6 +40,8 @@ EXPORTED = (
     "harp_mixed_expand", "harp_rotate_in_mixed", "harp_rotate_out_mixed",
     "harp_rotate_mixed_workspace_bytes",
     "harp_linear_fused_mixed", "harp_linear_mixed_workspace_bytes",
+    "harp_rmsnorm", "harp_rmsnorm_fp8", "harp_silu_mul_fp8", "harp_fp8_gemm",
+    "harp_fp8_gemm_grouped",
     "harp_status_string", "harp_last_hip_error",
 )
 
@@ -74,6 +76,11 @@ class harp_qweight(ctypes.Structure):
                 ("zero", c_void_p)]
 
 
+class harp_fp8_weight(ctypes.Structure):
+    _fields_ = [("N", c_int32), ("K", c_int32), ("experts", c_int32), ("w", c_void_p),
+                ("scale", c_void_p)]
+
+
 class harp_chain_layer(ctypes.Structure):
     _fields_ = [("V", harp_rotation), ("W", harp_qweight), ("U", harp_rotation),
                 ("y", c_void_p)]
@@ -92,6 +99,7 @@ def _load() -> ctypes.CDLL:
     R = ctypes.POINTER(harp_rotation)
     Q = ctypes.POINTER(harp_qweight)
     MR = ctypes.POINTER(harp_mixed_rotation)
+    F8 = ctypes.POINTER(harp_fp8_weight)
     sig = {
         "harp_rotate_in": (c_int32, [R, c_void_p, c_int32, c_void_p, c_int32, c_int32, c_void_p]),
         "harp_rotate_out": (c_int32, [R, c_void_p, c_void_p, c_int32, c_int32, c_void_p]),
@@ -128,6 +136,17 @@ def _load() -> ctypes.CDLL:
         "harp_linear_mixed_workspace_bytes": (c_size_t, [c_int32, c_int32, c_int32]),
         "harp_quantize_pack": (c_int32, [c_void_p, c_int32, c_int32, c_int32, c_void_p, c_void_p,
                                           c_void_p, c_void_p]),
+        "harp_rmsnorm": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_int32,
+                                   c_float, c_void_p, c_int32, c_int32, c_int32, c_void_p]),
+        "harp_rmsnorm_fp8": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_int32,
+                                       c_float, c_void_p, c_void_p, c_int32, c_int32,
+                                       c_void_p]),
+        "harp_silu_mul_fp8": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_int32,
+                                        c_void_p]),
+        "harp_fp8_gemm": (c_int32, [F8, c_void_p, c_void_p, c_void_p, c_int32, c_int32,
+                                    c_void_p]),
+        "harp_fp8_gemm_grouped": (c_int32, [F8, c_void_p, c_void_p, c_int32, c_void_p, c_void_p,
+                                            c_void_p, c_int32, c_int32, c_void_p]),
         "harp_status_string": (c_char_p, [c_int32]),
         "harp_last_hip_error": (c_int32, []),
     }
@@ -410,6 +429,126 @@ def harp_quantize_pack(Wp, bits: int, qweight, scale, zero, stream=None) -> None
     N, K = Wp.shape
     _check(lib.harp_quantize_pack(_ptr(Wp), N, K, bits, _ptr(qweight), _ptr(scale), _ptr(zero),
                                   _stream(stream)), "harp_quantize_pack")
+
+
+# 8-bit operators.  Their tensors are checked here as well (device, type,
+# shape, contiguous rows): the C entry points see plain addresses.
+
+def _fp8_dtypes():
+    torch = _torch()
+    return (torch.float8_e4m3fn, torch.uint8)
+
+
+def _runs(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _expect(name: str, t, shape, dtypes, device=None):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+
+
+def _call_on(device, stream, where, f, *args):
+    """Run f on the tensors' device (made current for the call) and stream."""
+    torch = _torch()
+    if device.type != "cuda":
+        raise ValueError(f"{where}: tensors on {device}, expected a GPU")
+    if device.index == torch.cuda.current_device():
+        _check(f(*args, _stream(stream)), where)
+    else:
+        with torch.cuda.device(device):
+            _check(f(*args, _stream(stream)), where)
+
+
+class FP8Weight:
+    """e4m3 weight: w float8_e4m3fn (or uint8 codes) [N][K] or [experts][N][K]
+    and scale float32 [ceil(N/128)][ceil(K/128)], with experts in front where
+    w has them."""
+
+    def __init__(self, w, scale):
+        torch = _torch()
+        if w.dim() not in (2, 3):
+            raise ValueError("w: [N][K] or [experts][N][K]")
+        self.experts = w.shape[0] if w.dim() == 3 else 1
+        self.N, self.K = w.shape[-2:]
+        _expect("w", w, w.shape, _fp8_dtypes())
+        _expect("scale", scale, (*w.shape[:-2], _runs(self.N), _runs(self.K)), (torch.float32,),
+                w.device)
+        self.w, self.scale, self.device = w, scale, w.device
+        self.c = harp_fp8_weight(self.N, self.K, self.experts, w.data_ptr(), scale.data_ptr())
+
+
+def _norm_inputs(x, weight, residual, residual_out):
+    if x.dim() != 2:
+        raise ValueError("x: [M][D]")
+    _expect("x", x, x.shape, (x.dtype,))
+    _expect("weight", weight, (x.shape[1],), (weight.dtype,), x.device)
+    for name, t in (("residual", residual), ("residual_out", residual_out)):
+        if t is not None:
+            _expect(name, t, x.shape, (x.dtype,), x.device)
+
+
+def harp_rmsnorm(x, weight, y, eps: float = 1e-6, residual=None, residual_out=None,
+                 stream=None) -> None:
+    """y = norm(x + residual) * weight for x [M][D], and residual_out = x + residual."""
+    _norm_inputs(x, weight, residual, residual_out)
+    _expect("y", y, x.shape, (y.dtype,), x.device)
+    _call_on(x.device, stream, "harp_rmsnorm", lib.harp_rmsnorm, x.data_ptr(), _dtype_code(x),
+             _ptr(residual), _ptr(residual_out), weight.data_ptr(), _dtype_code(weight), eps,
+             y.data_ptr(), _dtype_code(y), x.shape[0], x.shape[1])
+
+
+def harp_rmsnorm_fp8(x, weight, q, q_scale, eps: float = 1e-6, residual=None, residual_out=None,
+                     stream=None) -> None:
+    """harp_rmsnorm with its output as codes q [M][D] and q_scale [M][ceil(D/128)]."""
+    _norm_inputs(x, weight, residual, residual_out)
+    M, D = x.shape
+    _expect("q", q, x.shape, _fp8_dtypes(), x.device)
+    _expect("q_scale", q_scale, (M, _runs(D)), (_torch().float32,), x.device)
+    _call_on(x.device, stream, "harp_rmsnorm_fp8", lib.harp_rmsnorm_fp8, x.data_ptr(),
+             _dtype_code(x), _ptr(residual), _ptr(residual_out), weight.data_ptr(),
+             _dtype_code(weight), eps, q.data_ptr(), q_scale.data_ptr(), M, D)
+
+
+def harp_silu_mul_fp8(gate_up, q, q_scale, stream=None) -> None:
+    """Codes of silu(gate) * up for gate_up [M][2 D] (gates first)."""
+    M, D = q.shape
+    _expect("q", q, (M, D), _fp8_dtypes())
+    _expect("gate_up", gate_up, (M, 2 * D), (gate_up.dtype,), q.device)
+    _expect("q_scale", q_scale, (M, _runs(D)), (_torch().float32,), q.device)
+    _call_on(q.device, stream, "harp_silu_mul_fp8", lib.harp_silu_mul_fp8, gate_up.data_ptr(),
+             _dtype_code(gate_up), q.data_ptr(), q_scale.data_ptr(), M, D)
+
+
+def harp_fp8_gemm(W: FP8Weight, a, a_scale, y, stream=None) -> None:
+    """y [M][N] = W a for codes a [M][K] with a_scale [M][ceil(K/128)]."""
+    M = a.shape[0]
+    _expect("a", a, (M, W.K), _fp8_dtypes(), W.device)
+    _expect("a_scale", a_scale, (M, _runs(W.K)), (_torch().float32,), W.device)
+    _expect("y", y, (M, W.N), (y.dtype,), W.device)
+    _call_on(W.device, stream, "harp_fp8_gemm", lib.harp_fp8_gemm, ctypes.byref(W.c),
+             a.data_ptr(), a_scale.data_ptr(), y.data_ptr(), _dtype_code(y), M)
+
+
+def harp_fp8_gemm_grouped(W: FP8Weight, a, a_scale, offsets, y, rows=None, stream=None) -> None:
+    """y[i] = W_e a[rows[i]] for offsets[e] <= i < offsets[e + 1] (int32 device tensors)."""
+    torch = _torch()
+    a_rows, M = a.shape[0], y.shape[0]
+    _expect("a", a, (a_rows, W.K), _fp8_dtypes(), W.device)
+    _expect("a_scale", a_scale, (a_rows, _runs(W.K)), (torch.float32,), W.device)
+    _expect("offsets", offsets, (W.experts + 1,), (torch.int32,), W.device)
+    _expect("y", y, (M, W.N), (y.dtype,), W.device)
+    if rows is not None:
+        _expect("rows", rows, (M,), (torch.int32,), W.device)
+    _call_on(W.device, stream, "harp_fp8_gemm_grouped", lib.harp_fp8_gemm_grouped,
+             ctypes.byref(W.c), a.data_ptr(), a_scale.data_ptr(), a_rows, _ptr(rows),
+             offsets.data_ptr(), y.data_ptr(), _dtype_code(y), M)
 
 
 def harp_last_hip_error() -> int:

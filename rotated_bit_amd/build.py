@@ -25,7 +25,7 @@ LIB = os.path.join(HERE, "libharp.so")
 ARCH = os.environ.get("HARP_OFFLOAD_ARCH", "gfx950")
 
 HIP_SOURCES = ["rotate.hip", "mixed.hip", "gemv.hip", "gemv_f4.hip", "gemv_mc.hip", "skinny.hip", "skinny_wide.hip", "gemm.hip",
-               "dequant.hip", "prep.hip", "chain.hip", "harp_api.cpp"]
+               "dequant.hip", "prep.hip", "chain.hip", "norm_fp8.hip", "fp8_gemm.hip", "harp_api.cpp"]
 CXX_SOURCES = ["validate.cpp", "mixed_expand.cpp"]
 
 # Code object v5: loadable by the HIP runtime that ships inside torch, which

@@ -327,6 +327,53 @@ harp_status harp_linear_fused_mixed(const harp_mixed_rotation* V, const harp_qwe
   return from_hip(harp::launch_rotate_mixed(*U, yp, HARP_F32, y, y_dt, M, true, ys, s));
 }
 
+harp_status harp_rmsnorm(const void* x, harp_dtype x_dt, const void* residual,
+                         void* residual_out, const void* weight, harp_dtype w_dt, float eps,
+                         void* y, harp_dtype y_dt, int32_t M, int32_t D, harp_stream stream) {
+  const harp_status st = harp::validate_rmsnorm(x, x_dt, residual, residual_out, weight, w_dt,
+                                                eps, y, y_dt, false, nullptr, M, D);
+  if (st != HARP_OK || M == 0) return st;
+  return from_hip(harp::launch_rmsnorm(x, x_dt, residual, residual_out, weight, w_dt, eps, y,
+                                       y_dt, nullptr, M, D, as_stream(stream)));
+}
+
+harp_status harp_rmsnorm_fp8(const void* x, harp_dtype x_dt, const void* residual,
+                             void* residual_out, const void* weight, harp_dtype w_dt, float eps,
+                             uint8_t* q, float* q_scale, int32_t M, int32_t D,
+                             harp_stream stream) {
+  const harp_status st = harp::validate_rmsnorm(x, x_dt, residual, residual_out, weight, w_dt,
+                                                eps, q, 0, true, q_scale, M, D);
+  if (st != HARP_OK || M == 0) return st;
+  return from_hip(harp::launch_rmsnorm(x, x_dt, residual, residual_out, weight, w_dt, eps, q, 0,
+                                       q_scale, M, D, as_stream(stream)));
+}
+
+harp_status harp_silu_mul_fp8(const void* gate_up, harp_dtype x_dt, uint8_t* q, float* q_scale,
+                              int32_t M, int32_t D, harp_stream stream) {
+  const harp_status st = harp::validate_silu_mul_fp8(gate_up, x_dt, q, q_scale, M, D);
+  if (st != HARP_OK || M == 0) return st;
+  return from_hip(harp::launch_silu_mul_fp8(gate_up, x_dt, q, q_scale, M, D, as_stream(stream)));
+}
+
+harp_status harp_fp8_gemm(const harp_fp8_weight* W, const uint8_t* a, const float* a_scale,
+                          void* y, harp_dtype y_dt, int32_t M, harp_stream stream) {
+  const harp_status st = harp::validate_fp8_gemm(W, a, a_scale, y, y_dt, M);
+  if (st != HARP_OK || M == 0) return st;
+  return from_hip(harp::launch_fp8_gemm(*W, a, a_scale, M, nullptr, nullptr, y, y_dt, M,
+                                        as_stream(stream)));
+}
+
+harp_status harp_fp8_gemm_grouped(const harp_fp8_weight* W, const uint8_t* a,
+                                  const float* a_scale, int32_t a_rows, const int32_t* rows,
+                                  const int32_t* offsets, void* y, harp_dtype y_dt, int32_t M,
+                                  harp_stream stream) {
+  const harp_status st =
+      harp::validate_fp8_gemm_grouped(W, a, a_scale, a_rows, rows, offsets, y, y_dt, M);
+  if (st != HARP_OK || M == 0) return st;
+  return from_hip(harp::launch_fp8_gemm(*W, a, a_scale, a_rows, rows, offsets, y, y_dt, M,
+                                        as_stream(stream)));
+}
+
 harp_status harp_dequant(const harp_qweight* W, void* out, harp_dtype out_dt,
                          harp_stream stream) {
   const harp_status st = harp::validate_dequant(W, out, out_dt);

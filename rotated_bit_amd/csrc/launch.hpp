@@ -110,6 +110,20 @@ hipError_t launch_transpose(const float* in, float* out, int R, int C, hipStream
 hipError_t launch_quantize_pack(const float* wp, int N, int K, int bits, uint32_t* qw,
                                 uint16_t* sc, uint16_t* zr, hipStream_t stream);
 
+// Residual addition and RMS norm of M rows (norm_fp8.hip): y of y_dt, or
+// with q_scale non-null y holds the e4m3 codes.
+hipError_t launch_rmsnorm(const void* x, int x_dt, const void* residual, void* residual_out,
+                          const void* weight, int w_dt, float eps, void* y, int y_dt,
+                          float* q_scale, int M, int D, hipStream_t stream);
+// v = silu(gate) up of M rows as e4m3 codes.
+hipError_t launch_silu_mul_fp8(const void* gate_up, int x_dt, uint8_t* q, float* q_scale, int M,
+                               int D, hipStream_t stream);
+// The FP8 product (fp8_gemm.hip): offsets null: W's one matrix for all M
+// rows; otherwise grouped by expert, rows null for rows[i] = i.
+hipError_t launch_fp8_gemm(const harp_fp8_weight& W, const uint8_t* a, const float* a_scale,
+                           int a_rows, const int32_t* rows, const int32_t* offsets, void* y,
+                           int y_dt, int M, hipStream_t stream);
+
 // Dense w_hat [N][K], float32 or bf16.
 hipError_t launch_dequant(const harp_qweight& W, void* out, int out_dt,
                           hipStream_t stream);

@@ -420,6 +420,71 @@ harp_status validate_chain(const harp_chain_layer* layers, int32_t n_layers, con
   return HARP_OK;
 }
 
+harp_status check_fp8_weight(const harp_fp8_weight* W) {
+  if (W == nullptr || W->w == nullptr || W->scale == nullptr) return HARP_ERR_NULL;
+  if (W->N < 1 || W->N > HARP_MAX_DIM || W->K < 16 || W->K > HARP_MAX_DIM || W->K % 16 != 0 ||
+      W->experts < 1 || W->experts > HARP_MAX_EXPERTS)
+    return HARP_ERR_SHAPE;
+  if (!aligned(W->w, 16) || !aligned(W->scale, 16)) return HARP_ERR_ALIGN;
+  return HARP_OK;
+}
+
+harp_status validate_rmsnorm(const void* x, int x_dt, const void* residual,
+                             const void* residual_out, const void* weight, int w_dt, float eps,
+                             const void* y, int y_dt, bool fp8, const void* q_scale, int32_t M,
+                             int32_t D) {
+  if (residual == nullptr && residual_out != nullptr) return HARP_ERR_NULL;
+  if (D < 1 || D > HARP_MAX_NORM_DIM || (fp8 && D % 16 != 0)) return HARP_ERR_SHAPE;
+  if (!std::isfinite(eps) || eps < 0.0f) return HARP_ERR_SHAPE;
+  if (bad_dtype(x_dt) || bad_dtype(w_dt) || (!fp8 && bad_dtype(y_dt))) return HARP_ERR_DTYPE;
+  HARP_TRY(check_m(M));
+  HARP_TRY(check_data(x, M));
+  HARP_TRY(check_data(weight, M));
+  HARP_TRY(check_data(y, M));
+  if (fp8) HARP_TRY(check_data(q_scale, M));
+  if (!aligned(residual, 16) || !aligned(residual_out, 16)) return HARP_ERR_ALIGN;
+  return HARP_OK;
+}
+
+harp_status validate_silu_mul_fp8(const void* gate_up, int x_dt, const void* q,
+                                  const void* q_scale, int32_t M, int32_t D) {
+  if (D < 16 || D > HARP_MAX_DIM || D % 16 != 0) return HARP_ERR_SHAPE;
+  if (bad_dtype(x_dt)) return HARP_ERR_DTYPE;
+  HARP_TRY(check_m(M));
+  HARP_TRY(check_data(gate_up, M));
+  HARP_TRY(check_data(q, M));
+  HARP_TRY(check_data(q_scale, M));
+  return HARP_OK;
+}
+
+harp_status validate_fp8_gemm(const harp_fp8_weight* W, const void* a, const void* a_scale,
+                              const void* y, int y_dt, int32_t M) {
+  HARP_TRY(check_fp8_weight(W));
+  if (W->experts != 1) return HARP_ERR_SHAPE;
+  if (bad_dtype(y_dt)) return HARP_ERR_DTYPE;
+  HARP_TRY(check_m(M));
+  HARP_TRY(check_data(a, M));
+  HARP_TRY(check_data(a_scale, M));
+  HARP_TRY(check_data(y, M));
+  return HARP_OK;
+}
+
+harp_status validate_fp8_gemm_grouped(const harp_fp8_weight* W, const void* a,
+                                      const void* a_scale, int32_t a_rows, const void* rows,
+                                      const void* offsets, const void* y, int y_dt, int32_t M) {
+  HARP_TRY(check_fp8_weight(W));
+  if (bad_dtype(y_dt)) return HARP_ERR_DTYPE;
+  HARP_TRY(check_m(M));
+  if (a_rows < 0 || a_rows > HARP_MAX_M) return HARP_ERR_SHAPE;
+  if (M > 0 && (a_rows < 1 || (rows == nullptr && a_rows < M))) return HARP_ERR_SHAPE;
+  HARP_TRY(check_data(a, M));
+  HARP_TRY(check_data(a_scale, M));
+  HARP_TRY(check_data(offsets, M));
+  HARP_TRY(check_data(y, M));
+  if (!aligned(rows, 16)) return HARP_ERR_ALIGN;
+  return HARP_OK;
+}
+
 const char* status_string(harp_status s) {
   switch (s) {
     case HARP_OK: return "HARP_OK";

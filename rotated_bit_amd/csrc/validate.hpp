@@ -159,6 +159,22 @@ harp_status validate_chain(const harp_chain_layer* layers, int32_t n_layers, con
                            int x_dt, int y_dt, int32_t M, const void* workspace,
                            size_t ws_bytes);
 
+// 8-bit operators.
+harp_status check_fp8_weight(const harp_fp8_weight* W);
+// fp8: the checks of harp_rmsnorm_fp8 (y holds the codes, y_dt is not read);
+// otherwise those of harp_rmsnorm (q_scale is not read).
+harp_status validate_rmsnorm(const void* x, int x_dt, const void* residual,
+                             const void* residual_out, const void* weight, int w_dt, float eps,
+                             const void* y, int y_dt, bool fp8, const void* q_scale, int32_t M,
+                             int32_t D);
+harp_status validate_silu_mul_fp8(const void* gate_up, int x_dt, const void* q,
+                                  const void* q_scale, int32_t M, int32_t D);
+harp_status validate_fp8_gemm(const harp_fp8_weight* W, const void* a, const void* a_scale,
+                              const void* y, int y_dt, int32_t M);
+harp_status validate_fp8_gemm_grouped(const harp_fp8_weight* W, const void* a,
+                                      const void* a_scale, int32_t a_rows, const void* rows,
+                                      const void* offsets, const void* y, int y_dt, int32_t M);
+
 const char* status_string(harp_status s);
 
 }  // namespace harp
