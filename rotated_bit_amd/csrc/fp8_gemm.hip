@@ -177,6 +177,267 @@ __global__ __launch_bounds__(512) void fp8_stream_kernel(Fp8Args p) {
     store4(static_cast<YT*>(p.y) + static_cast<size_t>(t.row0 + c) * p.N, n0 + 4 * g, p.N, acc);
 }
 
+// ---- tiles through LDS --------------------------------------------------------
+//
+// BN outputs x BM rows per workgroup, WN x WM per wave, one run (128 inputs,
+// a 128-byte row of LDS) per step.  Two LDS buffers: while the waves work on
+// one, the next run's codes and row scales come in with buffer_load ... lds
+// (16 bytes per lane, no registers in between); one barrier per step.  A
+// buffer load past its descriptor's end writes zeros, which covers rows past
+// the tile and, with the offset pushed out of range, the inputs from K on.
+//
+// LDS rows hold their eight 16-byte chunks at chunk ^ key(row), so that the
+// eight lanes of a read phase hit eight different bank groups.  Matrix tile
+// i of 64 outputs takes the LDS rows 16 (r / 4) + 4 i + r % 4 (r = 0..15), so
+// that a lane's results over the four tiles are 16 consecutive outputs and
+// a row of y is written in whole 128-byte lines.
+__device__ __forceinline__ int w_key(int row) { return (row & 3) | ((row >> 2) & 4); }
+__device__ __forceinline__ int a_key(int row) { return row & 7; }
+
+// Descriptor of `bytes` bytes at p (raw, no stride); wave-uniform.
+__device__ __forceinline__ u32x4 buffer_of(const void* p, uint32_t bytes) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  return u32x4{static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(v))),
+               static_cast<uint32_t>(
+                   __builtin_amdgcn_readfirstlane(static_cast<int>((v >> 32) & 0xffff))),
+               static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(bytes))),
+               0x00020000u};
+}
+// 16 (4) bytes per lane from descriptor r at off to LDS address
+// lds + 16 (4) lane.  The s_nop covers the wait states between a vector
+// write of the descriptor's scalars, or the write of m0, and the load.
+__device__ __forceinline__ void load_lds16(u32x4 r, const uint32_t (&off)[4], uint32_t lds,
+                                           int step) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %5, 0 offen lds\n\t"
+      "s_add_u32 m0, m0, %6\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %5, 0 offen lds\n\t"
+      "s_add_u32 m0, m0, %6\n\ts_nop 0\n\tbuffer_load_dwordx4 %3, %5, 0 offen lds\n\t"
+      "s_add_u32 m0, m0, %6\n\ts_nop 0\n\tbuffer_load_dwordx4 %4, %5, 0 offen lds" ::"s"(lds),
+      "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "s"(r), "s"(step)
+      : "memory", "scc");
+}
+__device__ __forceinline__ void load_lds4(u32x4 r, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds),
+               "v"(off), "s"(r)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+      (const __attribute__((address_space(3))) void*)p));
+}
+
+// Sixteen consecutive outputs n .. n+15 of a row.
+__device__ __forceinline__ void store16(float* row, int n, int N, const floatx4 (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) store4(row, n + 4 * i, N, v[i]);
+}
+__device__ __forceinline__ void store16(uint16_t* row, int n, int N, const floatx4 (&v)[4]) {
+  if (N % 8 == 0) {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2)
+      if (n + 4 * i < N)
+        *reinterpret_cast<u32x4*>(row + n + 4 * i) =
+            u32x4{pack_bf16x2(v[i][0], v[i][1]), pack_bf16x2(v[i][2], v[i][3]),
+                  pack_bf16x2(v[i + 1][0], v[i + 1][1]), pack_bf16x2(v[i + 1][2], v[i + 1][3])};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) store4(row, n + 4 * i, N, v[i]);
+  }
+}
+
+// XCD-aware order: workgroup ids go round the 8 XCDs, so each XCD gets a
+// contiguous run of the tile order, in which panels of 4 output tiles run
+// over the row tiles: the 32 tiles an XCD works on at a time share 4 weight
+// and 8 row tiles in its L2.
+__device__ __forceinline__ void tile_of(int id, int n_tiles, int m_tiles, int& nt, int& mt) {
+  constexpr int kXcds = 8, kPanel = 4;
+  const int total = n_tiles * m_tiles;
+  const int per = total / kXcds, more = total % kXcds;
+  const int xcd = id % kXcds;
+  const int t = xcd * per + min(xcd, more) + id / kXcds;
+  const int panel = t / (kPanel * m_tiles);
+  const int width = min(kPanel, n_tiles - panel * kPanel);
+  const int r = t - panel * kPanel * m_tiles;
+  nt = panel * kPanel + r % width;
+  mt = r / width;
+}
+
+template <int BN, int BM, int WN, int WM, typename YT>
+__global__ __launch_bounds__(BN / WN * (BM / WM) * kWave) void fp8_tile_kernel(Fp8Args p,
+                                                                               int n_tiles,
+                                                                               int m_tiles) {
+  constexpr bool kExact = sizeof(YT) == 4;
+  constexpr int kWaves = BN / WN * (BM / WM);
+  constexpr int kRowsPerLoad = 8 * kWaves;      // 8 LDS rows per wave instruction
+  constexpr int kWLoads = BN / kRowsPerLoad, kALoads = BM / kRowsPerLoad;
+  static_assert(kWLoads == 4 && kALoads == 4 && kRowsPerLoad % 32 == 0, "four loads each");
+  static_assert(WN % 64 == 0 && kFp8Run % WN == 0 && WM % 16 == 0, "");
+  constexpr int kABase = BN * kFp8Run, kSBase = kABase + BM * kFp8Run;
+  constexpr int kStage = kSBase + BM * 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2][kStage];
+  int nt, mt;
+  tile_of(blockIdx.x, n_tiles, m_tiles, nt, mt);
+  Tile t;
+  if (!find_tile<BM>(p, mt, t)) return;
+  t.e = __builtin_amdgcn_readfirstlane(t.e);
+  t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
+  t.count = __builtin_amdgcn_readfirstlane(t.count);
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int n0 = nt * BN;
+  const int K = p.K, KB = p.KB;
+
+  // what this thread loads: LDS row lr + i kRowsPerLoad, chunk lane % 8
+  const int lr = 8 * wave + (lane >> 3);
+  const int wc = 16 * ((lane & 7) ^ w_key(lr)), ac = 16 * ((lane & 7) ^ a_key(lr));
+  uint32_t woff[kWLoads], aoff[kALoads];
+#pragma unroll
+  for (int i = 0; i < kWLoads; ++i) woff[i] = (lr + i * kRowsPerLoad) * K + wc;
+  const uint8_t* abase = p.a;
+  const float* sabase = p.as;
+  uint32_t abytes, sabytes;
+  constexpr uint32_t kOut = 0x80000000u;
+  const bool s_loader = static_cast<int>(threadIdx.x) < BM;   // whole waves
+  uint32_t soff = kOut;
+  if (p.rows == nullptr) {
+    abase += static_cast<size_t>(t.row0) * K;
+    sabase += static_cast<size_t>(t.row0) * KB;
+    abytes = t.count * K;
+    sabytes = t.count * KB * 4;
+#pragma unroll
+    for (int i = 0; i < kALoads; ++i) aoff[i] = (lr + i * kRowsPerLoad) * K + ac;
+    if (s_loader) soff = threadIdx.x * KB * 4;
+  } else {
+    abytes = static_cast<uint32_t>(p.a_rows) * K;       // below 2^31 (host)
+    sabytes = static_cast<uint32_t>(p.a_rows) * KB * 4;
+#pragma unroll
+    for (int i = 0; i < kALoads; ++i) {
+      const int r = lr + i * kRowsPerLoad;
+      const int src = r < t.count ? source_row(p, t.row0 + r) : -1;
+      aoff[i] = src < 0 ? kOut : static_cast<uint32_t>(src) * K + ac;
+    }
+    if (static_cast<int>(threadIdx.x) < min(BM, t.count)) {
+      const int src = source_row(p, t.row0 + threadIdx.x);
+      if (src >= 0) soff = static_cast<uint32_t>(src) * KB * 4;
+    }
+  }
+  const uint8_t* wbase = p.w + (static_cast<size_t>(t.e) * p.N + n0) * K;
+  const uint32_t wbytes = min(BN, p.N - n0) * K;
+  const int tail = K % kFp8Run;      // inputs of the last run, 0: all 128
+
+  auto load = [&](int kb) {
+    const uint32_t lds0 =
+        __builtin_amdgcn_readfirstlane(lds_address(lds[kb & 1])) + wave * 1024;
+    const int k = kb * kFp8Run;
+    const u32x4 rw = buffer_of(wbase + k, wbytes - k), ra = buffer_of(abase + k, abytes - k);
+    const bool cut = tail != 0 && kb == KB - 1;
+    const bool w_out = cut && wc >= tail, a_out = cut && ac >= tail;
+    if (cut) {   // once, after which the offsets are not used again
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        woff[i] = w_out ? kOut : woff[i];
+        aoff[i] = a_out ? kOut : aoff[i];
+      }
+    }
+    load_lds16(rw, woff, lds0, kRowsPerLoad * kFp8Run);
+    load_lds16(ra, aoff, lds0 + kABase, kRowsPerLoad * kFp8Run);
+    if (s_loader)
+      load_lds4(buffer_of(sabase + kb, sabytes - kb * 4), soff,
+                __builtin_amdgcn_readfirstlane(lds_address(lds[kb & 1])) + kSBase + wave * 256);
+  };
+
+  const int wn = (wave % (BN / WN)) * WN, wm = (wave / (BN / WN)) * WM;
+  const int g = lane >> 4, c = lane & 15;
+  const float* sw =
+      p.ws + (static_cast<size_t>(t.e) * fp8_runs(p.N) + min(n0 + wn, p.N - 1) / kFp8Run) * KB;
+  floatx4 acc[WN / 16][WM / 16];
+#pragma unroll
+  for (int i = 0; i < WN / 16; ++i)
+#pragma unroll
+    for (int j = 0; j < WM / 16; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  // fragment of LDS row `row` (16-byte chunks 2 g and 2 g + 1)
+  auto fragment = [&](const uint8_t* base, int row, int key) {
+    const u32x4 lo = *reinterpret_cast<const u32x4*>(base + row * kFp8Run + 16 * ((2 * g) ^ key));
+    const u32x4 hi =
+        *reinterpret_cast<const u32x4*>(base + row * kFp8Run + 16 * ((2 * g + 1) ^ key));
+    return i32x8{static_cast<int>(lo[0]), static_cast<int>(lo[1]), static_cast<int>(lo[2]),
+                 static_cast<int>(lo[3]), static_cast<int>(hi[0]), static_cast<int>(hi[1]),
+                 static_cast<int>(hi[2]), static_cast<int>(hi[3])};
+  };
+
+  load(0);
+  for (int kb = 0; kb < KB; ++kb) {
+    // this wave's part of run kb has arrived and it has read all of run
+    // kb - 1; after the barrier that holds for every wave
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (kb + 1 < KB) load(kb + 1);
+    const uint8_t* st = lds[kb & 1];
+    const float swk = sw[kb];
+    i32x8 fa[WM / 16];
+    float s[WM / 16];
+#pragma unroll
+    for (int j = 0; j < WM / 16; ++j) {
+      const int row = wm + 16 * j + c;
+      fa[j] = fragment(st + kABase, row, a_key(row));
+      s[j] = reinterpret_cast<const float*>(st + kSBase)[row] * swk;
+    }
+#pragma unroll
+    for (int i = 0; i < WN / 16; ++i) {
+      const int row = wn + 64 * (i / 4) + 16 * (c >> 2) + 4 * (i % 4) + (c & 3);
+      const i32x8 fw = fragment(st, row, w_key(row));
+#pragma unroll
+      for (int j = 0; j < WM / 16; ++j) {
+        const floatx4 P = mfma_run<kExact>(fw, fa[j]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(s[j], P[r], acc[i][j][r]);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < WM / 16; ++j) {
+    const int m = wm + 16 * j + c;
+    if (m >= t.count) continue;
+    YT* row = static_cast<YT*>(p.y) + static_cast<size_t>(t.row0 + m) * p.N;
+#pragma unroll
+    for (int i = 0; i < WN / 16; i += 4) {
+      const floatx4 v[4] = {acc[i][j], acc[i + 1][j], acc[i + 2][j], acc[i + 3][j]};
+      store16(row, n0 + wn + 16 * i + 16 * g, p.N, v);
+    }
+  }
+}
+
+template <int BN, int BM, int WN, int WM, typename YT>
+hipError_t launch_tile(const Fp8Args& p, int live, hipStream_t stream) {
+  const int n_tiles = (p.N + BN - 1) / BN;
+  const int m_tiles = static_cast<int>((p.M + static_cast<int64_t>(live) * (BM - 1)) / BM);
+  fp8_tile_kernel<BN, BM, WN, WM, YT>
+      <<<dim3(n_tiles * m_tiles), BN / WN * (BM / WM) * kWave, 0, stream>>>(p, n_tiles, m_tiles);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+namespace {
+
+template <typename YT>
+hipError_t launch_by_size(const Fp8Args& p, hipStream_t stream) {
+  // experts with rows; sum_e ceil(c_e / BM) <= (M + live (BM - 1)) / BM
+  const int live = p.offsets == nullptr ? 1 : (p.E < p.M ? p.E : p.M);
+  // the tiles' buffer offsets reach 2^31 bytes into a where rows are gathered
+  const bool reach = p.rows == nullptr || static_cast<int64_t>(p.a_rows) * p.K < (int64_t{1} << 31);
+  if (p.M > 64 * live && reach) {
+    if constexpr (sizeof(YT) == 4) return launch_tile<128, 128, 64, 64, YT>(p, live, stream);
+    if (p.M > 512 * live) return launch_tile<256, 256, 128, 64, YT>(p, live, stream);
+    return launch_tile<128, 128, 64, 64, YT>(p, live, stream);
+  }
+  const dim3 grid((p.N + 15) / 16, (p.M + live * 15) / 16);
+  fp8_stream_kernel<YT><<<grid, 512, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_fp8_gemm(const harp_fp8_weight& W, const uint8_t* a, const float* a_scale,
@@ -184,14 +445,8 @@ hipError_t launch_fp8_gemm(const harp_fp8_weight& W, const uint8_t* a, const flo
                            int y_dt, int M, hipStream_t stream) {
   const Fp8Args p{W.w, W.scale, a,   a_scale,        rows,      offsets, y,
                   W.N, W.K,     fp8_runs(W.K), W.experts, M,       a_rows};
-  // sum_e ceil(c_e / BM) <= (M + live (BM - 1)) / BM with live <= min(E, M)
-  const int live = offsets == nullptr ? 1 : (W.experts < M ? W.experts : M);
-  const dim3 grid((W.N + 15) / 16, (M + live * 15) / 16);
-  if (y_dt == HARP_BF16)
-    fp8_stream_kernel<uint16_t><<<grid, 512, 0, stream>>>(p);
-  else
-    fp8_stream_kernel<float><<<grid, 512, 0, stream>>>(p);
-  return hipGetLastError();
+  return y_dt == HARP_BF16 ? launch_by_size<uint16_t>(p, stream)
+                           : launch_by_size<float>(p, stream);
 }
 
 }  // namespace harp

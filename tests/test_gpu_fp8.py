@@ -341,6 +341,24 @@ def test_grouped_offsets_out_of_range_write_nothing_else(M):
     assert torch.all(big[:4] == 7.0) and torch.all(big[4 + M:] == 7.0)
 
 
+@pytest.mark.parametrize("M", [3, 100])
+def test_grouped_rows_past_two_gigabytes(M):
+    rng = np.random.default_rng(10)
+    N, K, a_rows = 48, 65536, 40000                       # a of 2.6e9 bytes
+    W, wq, ws = weight(rng, N, K, 1)
+    a = torch.zeros((a_rows, K), dtype=torch.uint8, device="cuda").view(E4)
+    sa = torch.zeros((a_rows, K // 128), device="cuda")
+    used = [0, 5, 32767, 32768, 39998, 39999]
+    u, su, uq, us = rows_of(rng, len(used), K)
+    a.view(torch.uint8)[used] = u.view(torch.uint8)
+    sa[used] = su
+    pick = rng.integers(0, len(used), M)
+    rows = torch.tensor(np.array(used)[pick], dtype=torch.int32, device="cuda")
+    y = torch.empty((M, N), device="cuda")
+    lib().harp_fp8_gemm_grouped(W, a, sa, sizes_to_offsets([M]), y, rows=rows)
+    check_product(y, *F.product(uq[pick], us[pick], wq[0], ws[0]), K, "f32")
+
+
 def test_empty_calls():
     H = lib()
     rng = np.random.default_rng(1)
