@@ -194,9 +194,8 @@ __global__ __launch_bounds__(512) void fp8_stream_kernel(Fp8Args p) {
 __device__ __forceinline__ int w_key(int row) { return (row & 3) | ((row >> 2) & 4); }
 __device__ __forceinline__ int a_key(int row) { return row & 7; }
 
-// Descriptor of `bytes` bytes at p (raw, no stride); wave-uniform.
-__device__ __forceinline__ u32x4 buffer_of(const void* p, uint32_t bytes) {
-  const uint64_t v = reinterpret_cast<uint64_t>(p);
+// Descriptor of `bytes` bytes at address v (raw, no stride); wave-uniform.
+__device__ __forceinline__ u32x4 buffer_of(uint64_t v, uint32_t bytes) {
   return u32x4{static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(v))),
                static_cast<uint32_t>(
                    __builtin_amdgcn_readfirstlane(static_cast<int>((v >> 32) & 0xffff))),
@@ -262,7 +261,7 @@ __device__ __forceinline__ void tile_of(int id, int n_tiles, int m_tiles, int& n
   mt = r / width;
 }
 
-template <int BN, int BM, int WN, int WM, typename YT>
+template <int BN, int BM, int WN, int WM, int STAGES, typename YT>
 __global__ __launch_bounds__(BN / WN * (BM / WM) * kWave) void fp8_tile_kernel(Fp8Args p,
                                                                                int n_tiles,
                                                                                int m_tiles) {
@@ -273,8 +272,12 @@ __global__ __launch_bounds__(BN / WN * (BM / WM) * kWave) void fp8_tile_kernel(F
   static_assert(kWLoads == 4 && kALoads == 4 && kRowsPerLoad % 32 == 0, "four loads each");
   static_assert(WN % 64 == 0 && kFp8Run % WN == 0 && WM % 16 == 0, "");
   constexpr int kABase = BN * kFp8Run, kSBase = kABase + BM * kFp8Run;
-  constexpr int kStage = kSBase + BM * 4;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2][kStage];
+  constexpr int kSwWave = BM / kWave;           // the wave that loads the weight scales
+  constexpr int kStage = kSBase + kWaves * kWave * 4;
+  constexpr int kAhead = STAGES - 1;            // runs in flight
+  constexpr int kLoads = kWLoads + kALoads + 1;   // of a wave per run
+  static_assert(kSwWave < kWaves && BN / kFp8Run <= kWave, "");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES][kStage];
   int nt, mt;
   tile_of(blockIdx.x, n_tiles, m_tiles, nt, mt);
   Tile t;
@@ -297,7 +300,8 @@ __global__ __launch_bounds__(BN / WN * (BM / WM) * kWave) void fp8_tile_kernel(F
   const float* sabase = p.as;
   uint32_t abytes, sabytes;
   constexpr uint32_t kOut = 0x80000000u;
-  const bool s_loader = static_cast<int>(threadIdx.x) < BM;   // whole waves
+  // the first waves load the row scales, wave kSwWave a scale per 128
+  // outputs, the others zeros (every wave counts the same loads)
   uint32_t soff = kOut;
   if (p.rows == nullptr) {
     abase += static_cast<size_t>(t.row0) * K;
@@ -306,7 +310,7 @@ __global__ __launch_bounds__(BN / WN * (BM / WM) * kWave) void fp8_tile_kernel(F
     sabytes = t.count * KB * 4;
 #pragma unroll
     for (int i = 0; i < kALoads; ++i) aoff[i] = (lr + i * kRowsPerLoad) * K + ac;
-    if (s_loader) soff = threadIdx.x * KB * 4;
+    if (wave < kSwWave) soff = threadIdx.x * KB * 4;
   } else {
     abytes = static_cast<uint32_t>(p.a_rows) * K;       // below 2^31 (host)
     sabytes = static_cast<uint32_t>(p.a_rows) * KB * 4;
@@ -323,33 +327,42 @@ __global__ __launch_bounds__(BN / WN * (BM / WM) * kWave) void fp8_tile_kernel(F
   }
   const uint8_t* wbase = p.w + (static_cast<size_t>(t.e) * p.N + n0) * K;
   const uint32_t wbytes = min(BN, p.N - n0) * K;
+  if (wave == kSwWave) {
+    const int blocks = fp8_runs(p.N), b0 = n0 / kFp8Run;
+    sabase = p.ws + (static_cast<size_t>(t.e) * blocks + b0) * KB;
+    sabytes = min(BN / kFp8Run, blocks - b0) * KB * 4;
+    soff = lane < BN / kFp8Run ? lane * KB * 4 : kOut;
+  }
   const int tail = K % kFp8Run;      // inputs of the last run, 0: all 128
 
-  auto load = [&](int kb) {
-    const uint32_t lds0 =
-        __builtin_amdgcn_readfirstlane(lds_address(lds[kb & 1])) + wave * 1024;
-    const int k = kb * kFp8Run;
-    const u32x4 rw = buffer_of(wbase + k, wbytes - k), ra = buffer_of(abase + k, abytes - k);
-    const bool cut = tail != 0 && kb == KB - 1;
-    const bool w_out = cut && wc >= tail, a_out = cut && ac >= tail;
-    if (cut) {   // once, after which the offsets are not used again
+  const uint32_t lds_base = __builtin_amdgcn_readfirstlane(lds_address(lds)) + wave * 1024;
+  const uint32_t lds_scales = lds_base - wave * 1024 + kSBase + wave * 256;
+  // the next run to load: its bases and the bytes behind them
+  uint64_t wp = reinterpret_cast<uint64_t>(wbase), ap = reinterpret_cast<uint64_t>(abase),
+           sp = reinterpret_cast<uint64_t>(sabase);
+  uint32_t wleft = wbytes, aleft = abytes, sleft = sabytes;
+  auto load = [&](int kb, int stage) {
+    if (tail != 0 && kb == KB - 1) {   // the last load: inputs from K on read as zeros
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        woff[i] = w_out ? kOut : woff[i];
-        aoff[i] = a_out ? kOut : aoff[i];
+        woff[i] = wc >= tail ? kOut : woff[i];
+        aoff[i] = ac >= tail ? kOut : aoff[i];
       }
     }
-    load_lds16(rw, woff, lds0, kRowsPerLoad * kFp8Run);
-    load_lds16(ra, aoff, lds0 + kABase, kRowsPerLoad * kFp8Run);
-    if (s_loader)
-      load_lds4(buffer_of(sabase + kb, sabytes - kb * 4), soff,
-                __builtin_amdgcn_readfirstlane(lds_address(lds[kb & 1])) + kSBase + wave * 256);
+    const uint32_t at = stage * kStage;
+    load_lds16(buffer_of(wp, wleft), woff, lds_base + at, kRowsPerLoad * kFp8Run);
+    load_lds16(buffer_of(ap, aleft), aoff, lds_base + at + kABase, kRowsPerLoad * kFp8Run);
+    load_lds4(buffer_of(sp, sleft), soff, lds_scales + at);
+    wp += kFp8Run;
+    ap += kFp8Run;
+    sp += 4;
+    wleft -= kFp8Run;
+    aleft -= kFp8Run;
+    sleft -= 4;
   };
 
   const int wn = (wave % (BN / WN)) * WN, wm = (wave / (BN / WN)) * WM;
   const int g = lane >> 4, c = lane & 15;
-  const float* sw =
-      p.ws + (static_cast<size_t>(t.e) * fp8_runs(p.N) + min(n0 + wn, p.N - 1) / kFp8Run) * KB;
   floatx4 acc[WN / 16][WM / 16];
 #pragma unroll
   for (int i = 0; i < WN / 16; ++i)
@@ -366,34 +379,56 @@ __global__ __launch_bounds__(BN / WN * (BM / WM) * kWave) void fp8_tile_kernel(F
                  static_cast<int>(hi[2]), static_cast<int>(hi[3])};
   };
 
-  load(0);
+  constexpr int TI = WN / 16, TJ = WM / 16;
+  auto w_fragment = [&](const uint8_t* st, int i) {
+    const int row = wn + 64 * (i / 4) + 16 * (c >> 2) + 4 * (i % 4) + (c & 3);
+    return fragment(st, row, w_key(row));
+  };
+  for (int kb = 0; kb < min(kAhead, KB); ++kb) load(kb, kb);
+  int stage = 0;
   for (int kb = 0; kb < KB; ++kb) {
-    // this wave's part of run kb has arrived and it has read all of run
-    // kb - 1; after the barrier that holds for every wave
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    // this wave's part of run kb has arrived (the later runs may still be
+    // in flight) and it has read all of run kb - 1; after the barrier that
+    // holds for every wave
+    if (kb + kAhead <= KB)
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((kAhead - 1) * kLoads) : "memory");
+    else
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (kb + 1 < KB) load(kb + 1);
-    const uint8_t* st = lds[kb & 1];
-    const float swk = sw[kb];
-    i32x8 fa[WM / 16];
-    float s[WM / 16];
+    if (kb + kAhead < KB) load(kb + kAhead, stage == 0 ? STAGES - 1 : stage - 1);
+    const uint8_t* st = lds[stage];
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
+    const float* sc = reinterpret_cast<const float*>(st + kSBase);
+    i32x8 fa[TJ], fw[2];
+    float s[TJ];
+    fw[0] = w_fragment(st, 0);
+    const float swk = sc[BM + wn / kFp8Run];
 #pragma unroll
-    for (int j = 0; j < WM / 16; ++j) {
+    for (int j = 0; j < TJ; ++j) {
       const int row = wm + 16 * j + c;
       fa[j] = fragment(st + kABase, row, a_key(row));
-      s[j] = reinterpret_cast<const float*>(st + kSBase)[row] * swk;
+      s[j] = sc[row] * swk;
     }
+    // the scaled addition of a product comes kLag products after its issue:
+    // by then the matrix pipe has finished it and works on the later ones
+    constexpr int kLag = kExact ? 1 : 3;
+    floatx4 P[kLag + 1];
 #pragma unroll
-    for (int i = 0; i < WN / 16; ++i) {
-      const int row = wn + 64 * (i / 4) + 16 * (c >> 2) + 4 * (i % 4) + (c & 3);
-      const i32x8 fw = fragment(st, row, w_key(row));
-#pragma unroll
-      for (int j = 0; j < WM / 16; ++j) {
-        const floatx4 P = mfma_run<kExact>(fw, fa[j]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(s[j], P[r], acc[i][j][r]);
+    for (int q = 0; q < TI * TJ + kLag; ++q) {
+      const int i = q / TJ, j = q % TJ;
+      if (q < TI * TJ) {
+        if (j == 0 && i + 1 < TI) fw[(i + 1) & 1] = w_fragment(st, i + 1);
+        P[q % (kLag + 1)] = mfma_run<kExact>(fw[i & 1], fa[j]);
       }
+      if constexpr (!kExact) __builtin_amdgcn_sched_barrier(0);
+      if (q >= kLag) {
+        const int pi = (q - kLag) / TJ, pj = (q - kLag) % TJ;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[pi][pj][r] = fmaf(s[pj], P[(q - kLag) % (kLag + 1)][r], acc[pi][pj][r]);
+      }
+      if constexpr (!kExact) __builtin_amdgcn_sched_barrier(0);
     }
   }
 #pragma unroll
@@ -409,11 +444,11 @@ __global__ __launch_bounds__(BN / WN * (BM / WM) * kWave) void fp8_tile_kernel(F
   }
 }
 
-template <int BN, int BM, int WN, int WM, typename YT>
+template <int BN, int BM, int WN, int WM, int STAGES, typename YT>
 hipError_t launch_tile(const Fp8Args& p, int live, hipStream_t stream) {
   const int n_tiles = (p.N + BN - 1) / BN;
   const int m_tiles = static_cast<int>((p.M + static_cast<int64_t>(live) * (BM - 1)) / BM);
-  fp8_tile_kernel<BN, BM, WN, WM, YT>
+  fp8_tile_kernel<BN, BM, WN, WM, STAGES, YT>
       <<<dim3(n_tiles * m_tiles), BN / WN * (BM / WM) * kWave, 0, stream>>>(p, n_tiles, m_tiles);
   return hipGetLastError();
 }
@@ -429,9 +464,10 @@ hipError_t launch_by_size(const Fp8Args& p, hipStream_t stream) {
   // the tiles' buffer offsets reach 2^31 bytes into a where rows are gathered
   const bool reach = p.rows == nullptr || static_cast<int64_t>(p.a_rows) * p.K < (int64_t{1} << 31);
   if (p.M > 64 * live && reach) {
-    if constexpr (sizeof(YT) == 4) return launch_tile<128, 128, 64, 64, YT>(p, live, stream);
-    if (p.M > 512 * live) return launch_tile<256, 256, 128, 64, YT>(p, live, stream);
-    return launch_tile<128, 128, 64, 64, YT>(p, live, stream);
+    if constexpr (sizeof(YT) == 2) {
+      if (p.M > 512 * live) return launch_tile<256, 256, 128, 64, 2, YT>(p, live, stream);
+    }
+    return launch_tile<128, 128, 64, 64, 4, YT>(p, live, stream);
   }
   const dim3 grid((p.N + 15) / 16, (p.M + live * 15) / 16);
   fp8_stream_kernel<YT><<<grid, 512, 0, stream>>>(p);
