@@ -187,12 +187,13 @@ __global__ __launch_bounds__(512) void fp8_stream_kernel(Fp8Args p) {
 // the tile and, with the offset pushed out of range, the inputs from K on.
 //
 // LDS rows hold their eight 16-byte chunks at chunk ^ key(row), so that the
-// eight lanes of a read phase hit eight different bank groups.  Matrix tile
+// 16 lanes that read 16 bytes each at a time, from 16 rows, hit all 64 banks
+// (two rows' chunk slots): rows of one parity have eight keys.  Matrix tile
 // i of 64 outputs takes the LDS rows 16 (r / 4) + 4 i + r % 4 (r = 0..15), so
 // that a lane's results over the four tiles are 16 consecutive outputs and
 // a row of y is written in whole 128-byte lines.
-__device__ __forceinline__ int w_key(int row) { return (row & 3) | ((row >> 2) & 4); }
-__device__ __forceinline__ int a_key(int row) { return row & 7; }
+__device__ __forceinline__ int w_key(int row) { return ((row >> 1) & 1) | ((row >> 3) & 6); }
+__device__ __forceinline__ int a_key(int row) { return (row >> 1) & 7; }
 
 // Descriptor of `bytes` bytes at address v (raw, no stride); wave-uniform.
 __device__ __forceinline__ u32x4 buffer_of(uint64_t v, uint32_t bytes) {
@@ -205,15 +206,10 @@ __device__ __forceinline__ u32x4 buffer_of(uint64_t v, uint32_t bytes) {
 // 16 (4) bytes per lane from descriptor r at off to LDS address
 // lds + 16 (4) lane.  The s_nop covers the wait states between a vector
 // write of the descriptor's scalars, or the write of m0, and the load.
-__device__ __forceinline__ void load_lds16(u32x4 r, const uint32_t (&off)[4], uint32_t lds,
-                                           int step) {
-  asm volatile(
-      "s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %5, 0 offen lds\n\t"
-      "s_add_u32 m0, m0, %6\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %5, 0 offen lds\n\t"
-      "s_add_u32 m0, m0, %6\n\ts_nop 0\n\tbuffer_load_dwordx4 %3, %5, 0 offen lds\n\t"
-      "s_add_u32 m0, m0, %6\n\ts_nop 0\n\tbuffer_load_dwordx4 %4, %5, 0 offen lds" ::"s"(lds),
-      "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "s"(r), "s"(step)
-      : "memory", "scc");
+__device__ __forceinline__ void load_lds16(u32x4 r, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds),
+               "v"(off), "s"(r)
+               : "memory");
 }
 __device__ __forceinline__ void load_lds4(u32x4 r, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds),
@@ -292,10 +288,11 @@ __global__ __launch_bounds__(BN / WN * (BM / WM) * kWave) void fp8_tile_kernel(F
 
   // what this thread loads: LDS row lr + i kRowsPerLoad, chunk lane % 8
   const int lr = 8 * wave + (lane >> 3);
-  const int wc = 16 * ((lane & 7) ^ w_key(lr)), ac = 16 * ((lane & 7) ^ a_key(lr));
+  const int ac = 16 * ((lane & 7) ^ a_key(lr));
+  auto wc = [&](int i) { return 16 * ((lane & 7) ^ w_key(lr + i * kRowsPerLoad)); };
   uint32_t woff[kWLoads], aoff[kALoads];
 #pragma unroll
-  for (int i = 0; i < kWLoads; ++i) woff[i] = (lr + i * kRowsPerLoad) * K + wc;
+  for (int i = 0; i < kWLoads; ++i) woff[i] = (lr + i * kRowsPerLoad) * K + wc(i);
   const uint8_t* abase = p.a;
   const float* sabase = p.as;
   uint32_t abytes, sabytes;
@@ -341,24 +338,35 @@ __global__ __launch_bounds__(BN / WN * (BM / WM) * kWave) void fp8_tile_kernel(F
   uint64_t wp = reinterpret_cast<uint64_t>(wbase), ap = reinterpret_cast<uint64_t>(abase),
            sp = reinterpret_cast<uint64_t>(sabase);
   uint32_t wleft = wbytes, aleft = abytes, sleft = sabytes;
-  auto load = [&](int kb, int stage) {
-    if (tail != 0 && kb == KB - 1) {   // the last load: inputs from K on read as zeros
+  auto cut = [&]() {   // the last run: inputs from K on read as zeros
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        woff[i] = wc >= tail ? kOut : woff[i];
-        aoff[i] = ac >= tail ? kOut : aoff[i];
-      }
+    for (int i = 0; i < 4; ++i) {
+      woff[i] = wc(i) >= tail ? kOut : woff[i];
+      aoff[i] = ac >= tail ? kOut : aoff[i];
     }
+  };
+  // load n (0 .. kLoads - 1) of the next run into `stage`
+  auto load = [&](int n, int stage) {
     const uint32_t at = stage * kStage;
-    load_lds16(buffer_of(wp, wleft), woff, lds_base + at, kRowsPerLoad * kFp8Run);
-    load_lds16(buffer_of(ap, aleft), aoff, lds_base + at + kABase, kRowsPerLoad * kFp8Run);
-    load_lds4(buffer_of(sp, sleft), soff, lds_scales + at);
+    if (n < kWLoads)
+      load_lds16(buffer_of(wp, wleft), woff[n],
+                 lds_base + at + n * (kRowsPerLoad * kFp8Run));
+    else if (n < kWLoads + kALoads)
+      load_lds16(buffer_of(ap, aleft), aoff[n - kWLoads],
+                 lds_base + at + kABase + (n - kWLoads) * (kRowsPerLoad * kFp8Run));
+    else
+      load_lds4(buffer_of(sp, sleft), soff, lds_scales + at);
+  };
+  // moves on to run kb; from KB on the descriptors are empty and the loads
+  // only write zeros
+  auto advance = [&](int kb) {
     wp += kFp8Run;
     ap += kFp8Run;
     sp += 4;
-    wleft -= kFp8Run;
-    aleft -= kFp8Run;
-    sleft -= 4;
+    wleft = kb < KB ? wleft - kFp8Run : 0;
+    aleft = kb < KB ? aleft - kFp8Run : 0;
+    sleft = kb < KB ? sleft - 4 : 0;
+    if (tail != 0 && kb == KB - 1) cut();
   };
 
   const int wn = (wave % (BN / WN)) * WN, wm = (wave / (BN / WN)) * WM;
@@ -384,53 +392,95 @@ __global__ __launch_bounds__(BN / WN * (BM / WM) * kWave) void fp8_tile_kernel(F
     const int row = wn + 64 * (i / 4) + 16 * (c >> 2) + 4 * (i % 4) + (c & 3);
     return fragment(st, row, w_key(row));
   };
-  for (int kb = 0; kb < min(kAhead, KB); ++kb) load(kb, kb);
+  if (tail != 0 && KB == 1) cut();
+  for (int kb = 0; kb < kAhead; ++kb) {
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) load(n, kb);
+    advance(kb + 1);
+  }
+  // Step kb: the products of run kb - 1 that are left (its last two weight
+  // rows of tiles), under which the first operands of run kb are read, then
+  // run kb up to its own last two rows.  All reads of a run are thus done
+  // before the barrier that ends the step it began in, the loads of a run
+  // have that whole step to arrive, and the matrix pipe does not wait for
+  // LDS behind the barrier.
+  constexpr int kRows = 2, kRest = kRows * TJ, kProducts = TI * TJ;
+  // the scaled addition of a product comes kLag products after its issue: by
+  // then the matrix pipe has finished it and works on the later ones
+  constexpr int kLag = kExact ? 1 : 3;
+  // a load per kEvery products: issued in one go the loads fill the address
+  // queue and hold up the wave's matrix instructions
+  constexpr int kEvery = kProducts >= 2 * kLoads ? 2 : 1;
+  static_assert(kProducts >= kEvery * kLoads && TI % 4 == 0, "every load has a place");
+  i32x8 fa[TJ], fw[4];       // row i of weight tiles in fw[i % 4]
+  float s_old[TJ], s[TJ];
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) {
+    fa[j] = i32x8{};
+    s[j] = 0.0f;
+  }
+  fw[2] = fw[3] = i32x8{};
   int stage = 0;
+  floatx4 P[kLag + 1];
+  // product n of a step: the remaining rows column by column, so that each
+  // column's fa is free for the next run early, then the rows in order
+  auto row_of = [](int n) { return n < kRest ? TI - kRows + n % kRows : (n - kRest) / TJ; };
+  auto col_of = [](int n) { return n < kRest ? n / kRows : (n - kRest) % TJ; };
+  auto add = [&](int n) {
+    const int i = row_of(n), j = col_of(n);
+    const float f = n < kRest ? s_old[j] : s[j];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(f, P[n % (kLag + 1)][r], acc[i][j][r]);
+    asm volatile("" : "+v"(acc[i][j]));   // here, not at the end of the step
+  };
   for (int kb = 0; kb < KB; ++kb) {
-    // this wave's part of run kb has arrived (the later runs may still be
-    // in flight) and it has read all of run kb - 1; after the barrier that
+    // this wave's loads of run kb have arrived (later runs' may still be in
+    // flight) and its reads of run kb - 1 are done; after the barrier that
     // holds for every wave
-    if (kb + kAhead <= KB)
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((kAhead - 1) * kLoads) : "memory");
-    else
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((kAhead - 1) * kLoads) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (kb + kAhead < KB) load(kb + kAhead, stage == 0 ? STAGES - 1 : stage - 1);
     const uint8_t* st = lds[stage];
+    const int next = stage == 0 ? STAGES - 1 : stage - 1;
     stage = stage + 1 == STAGES ? 0 : stage + 1;
     const float* sc = reinterpret_cast<const float*>(st + kSBase);
-    i32x8 fa[TJ], fw[2];
-    float s[TJ];
-    fw[0] = w_fragment(st, 0);
     const float swk = sc[BM + wn / kFp8Run];
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
-      const int row = wm + 16 * j + c;
-      fa[j] = fragment(st + kABase, row, a_key(row));
-      s[j] = sc[row] * swk;
+      s_old[j] = s[j];
+      s[j] = sc[wm + 16 * j + c];
     }
-    // the scaled addition of a product comes kLag products after its issue:
-    // by then the matrix pipe has finished it and works on the later ones
-    constexpr int kLag = kExact ? 1 : 3;
-    floatx4 P[kLag + 1];
 #pragma unroll
-    for (int q = 0; q < TI * TJ + kLag; ++q) {
-      const int i = q / TJ, j = q % TJ;
-      if (q < TI * TJ) {
-        if (j == 0 && i + 1 < TI) fw[(i + 1) & 1] = w_fragment(st, i + 1);
-        P[q % (kLag + 1)] = mfma_run<kExact>(fw[i & 1], fa[j]);
+    for (int n = 0; n < kProducts; ++n) {
+      const int i = row_of(n), j = col_of(n);
+      if (n < 2) fw[n] = w_fragment(st, n);
+      if (n >= kRest && j == 0) fw[(i + 2) % 4] = w_fragment(st, i + 2);
+      P[n % (kLag + 1)] = mfma_run<kExact>(fw[i % 4], fa[j]);
+      if (n < kRest && n % kRows == kRows - 1) {
+        const int row = wm + 16 * j + c;
+        fa[j] = fragment(st + kABase, row, a_key(row));
       }
+      if (n == kRest) {
+#pragma unroll
+        for (int u = 0; u < TJ; ++u) s[u] *= swk;
+      }
+      if (n % kEvery == kEvery - 1 && n / kEvery < kLoads) load(n / kEvery, next);
       if constexpr (!kExact) __builtin_amdgcn_sched_barrier(0);
-      if (q >= kLag) {
-        const int pi = (q - kLag) / TJ, pj = (q - kLag) % TJ;
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          acc[pi][pj][r] = fmaf(s[pj], P[(q - kLag) % (kLag + 1)][r], acc[pi][pj][r]);
-      }
+      if (n >= kLag) add(n - kLag);
       if constexpr (!kExact) __builtin_amdgcn_sched_barrier(0);
     }
+#pragma unroll
+    for (int n = kProducts - kLag; n < kProducts; ++n) add(n);
+    advance(kb + kAhead + 1);
   }
+#pragma unroll
+  for (int n = 0; n < kRest; ++n) {
+    const int i = row_of(n), j = col_of(n);
+    const floatx4 D = mfma_run<kExact>(fw[i % 4], fa[j]);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(s[j], D[r], acc[i][j][r]);
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no load outlives its LDS
 #pragma unroll
   for (int j = 0; j < WM / 16; ++j) {
     const int m = wm + 16 * j + c;
