@@ -35,6 +35,10 @@ HIP_FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-command-line-argument",
 ]
+# Matrix results in vector registers: with one wave per SIMD the compiler
+# otherwise puts them in accumulation registers, and the scaled addition
+# that follows each product costs a move per value.
+SOURCE_FLAGS = {"fp8_gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 CXX_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall"]
 
 
@@ -73,7 +77,7 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
     for src in HIP_SOURCES:
         obj = os.path.join(BUILD, src + ".o")
         objs.append(obj)
-        cmds.append([cc, "-c", *HIP_FLAGS, "-o", obj, os.path.join(CSRC, src)])
+        cmds.append([cc, "-c", *HIP_FLAGS, *SOURCE_FLAGS.get(src, []), "-o", obj, os.path.join(CSRC, src)])
     for src in CXX_SOURCES:
         obj = os.path.join(BUILD, src + ".o")
         objs.append(obj)
