@@ -567,6 +567,8 @@ harp_status harp_fp8_gemm(const harp_fp8_weight *W, const uint8_t *a, const floa
  * for each as a router chose: for offsets[e] <= i < offsets[e + 1]
  *     y[i] = W_e a[rows[i]].
  *   a        [a_rows][W->K] codes;  a_scale [a_rows][ceil(K/128)] float32
+ *            (with rows, a_rows K at most 2^32 - 256 bytes:
+ *            HARP_ERR_UNSUPPORTED beyond)
  *   rows     [M] int32, or NULL for rows[i] = i (then a_rows >= M).  The same
  *            row may occur any number of times.  An entry outside
  *            [0, a_rows) makes its output row zero.

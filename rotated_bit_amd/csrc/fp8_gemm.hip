@@ -9,8 +9,11 @@
 // four fused multiply-adds per lane.  The weights are the row operand and a
 // the column operand: lane l holds the four consecutive outputs
 // n0 + 4 (l / 16) + 0..3 of row m0 + l % 16, which share one factor sa sw.
+#include <type_traits>
+
 #include "fp8_common.hpp"
 #include "launch.hpp"
+#include "validate.hpp"
 
 namespace harp {
 namespace {
@@ -79,16 +82,6 @@ __device__ __forceinline__ int source_row(const Fp8Args& p, int i) {
   return r >= 0 && r < p.a_rows ? r : -1;
 }
 
-// 32 codes of a row at inputs k .. k+31 (zeros from K on, and for !in).
-__device__ __forceinline__ i32x8 load_codes(const uint8_t* row, int k, int K, bool in) {
-  u32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
-  if (in && k + 16 <= K) lo = *reinterpret_cast<const u32x4*>(row + k);
-  if (in && k + 32 <= K) hi = *reinterpret_cast<const u32x4*>(row + k + 16);
-  return i32x8{static_cast<int>(lo[0]), static_cast<int>(lo[1]), static_cast<int>(lo[2]),
-               static_cast<int>(lo[3]), static_cast<int>(hi[0]), static_cast<int>(hi[1]),
-               static_cast<int>(hi[2]), static_cast<int>(hi[3])};
-}
-
 // Eight codes as bf16 (exact).
 __device__ __forceinline__ bf16x8 codes_bf16(int lo, int hi) {
   const bf16x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
@@ -142,61 +135,43 @@ __device__ __forceinline__ void store4(uint16_t* row, int n, int N, floatx4 v) {
   }
 }
 
-// One workgroup: 16 outputs of up to 16 rows; wave v sums the runs v, v + 8,
-// ..., and the eight sums meet in LDS.
-template <typename YT>
-__global__ __launch_bounds__(512) void fp8_stream_kernel(Fp8Args p) {
-  constexpr bool kExact = sizeof(YT) == 4;
-  __shared__ floatx4 part[8][kWave];
-  Tile t;
-  if (!find_tile<16>(p, blockIdx.y, t)) return;
-  const int lane = threadIdx.x & (kWave - 1);
-  const int wave = threadIdx.x / kWave;
-  const int n0 = blockIdx.x * 16, g = lane >> 4, c = lane & 15;
-  const int src = c < t.count ? source_row(p, t.row0 + c) : -1;
-  const size_t arow = src < 0 ? 0 : src;
-  const uint8_t* a = p.a + arow * p.K;
-  const float* sa = p.as + arow * p.KB;
-  const bool w_in = n0 + c < p.N;
-  const uint8_t* w = p.w + (static_cast<size_t>(t.e) * p.N + (w_in ? n0 + c : 0)) * p.K;
-  const float* sw = p.ws + (static_cast<size_t>(t.e) * fp8_runs(p.N) + n0 / kFp8Run) * p.KB;
-  floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int kb = wave; kb < p.KB; kb += 8) {
-    const int k = kb * kFp8Run + 32 * g;
-    const floatx4 P = mfma_run<kExact>(load_codes(w, k, p.K, w_in), load_codes(a, k, p.K, src >= 0));
-    const float s = src >= 0 ? sa[kb] * sw[kb] : 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = fmaf(s, P[i], acc[i]);
-  }
-  part[wave][lane] = acc;
-  __syncthreads();
-  if (wave != 0) return;
-#pragma unroll
-  for (int v = 1; v < 8; ++v) acc += part[v][lane];
-  if (c < t.count)
-    store4(static_cast<YT*>(p.y) + static_cast<size_t>(t.row0 + c) * p.N, n0 + 4 * g, p.N, acc);
+// A buffer offset past the end of every descriptor used here: those are at
+// most kFp8MaxGather bytes (gathered rows) or 256 rows of K.
+constexpr uint32_t kOut = kFp8MaxGather;
+
+__device__ __forceinline__ i32x8 join(u32x4 lo, u32x4 hi) {
+  return i32x8{static_cast<int>(lo[0]), static_cast<int>(lo[1]), static_cast<int>(lo[2]),
+               static_cast<int>(lo[3]), static_cast<int>(hi[0]), static_cast<int>(hi[1]),
+               static_cast<int>(hi[2]), static_cast<int>(hi[3])};
 }
 
 // ---- tiles through LDS --------------------------------------------------------
 //
 // BN outputs x BM rows per workgroup, WN x WM per wave, one run (128 inputs,
-// a 128-byte row of LDS) per step.  Two LDS buffers: while the waves work on
-// one, the next run's codes and row scales come in with buffer_load ... lds
-// (16 bytes per lane, no registers in between); one barrier per step.  A
-// buffer load past its descriptor's end writes zeros, which covers rows past
-// the tile and, with the offset pushed out of range, the inputs from K on.
+// a 128-byte row of LDS) per step of a group of waves.  KG groups take the
+// runs in turn and meet at the end (for few tiles: more waves per tile and
+// fewer steps).  STAGES LDS buffers per group: while the waves work on one,
+// the next runs' codes and scales come in with buffer_load ... lds (16 bytes
+// per lane, no registers in between); one barrier per step.  A buffer load
+// past its descriptor's end writes zeros, which covers rows past the tile
+// and, with the offset pushed out of range, the inputs from K on.
 //
 // LDS rows hold their eight 16-byte chunks at chunk ^ key(row), so that the
 // 16 lanes that read 16 bytes each at a time, from 16 rows, hit all 64 banks
-// (two rows' chunk slots): rows of one parity have eight keys.  Matrix tile
-// i of 64 outputs takes the LDS rows 16 (r / 4) + 4 i + r % 4 (r = 0..15), so
-// that a lane's results over the four tiles are 16 consecutive outputs and
-// a row of y is written in whole 128-byte lines.
-__device__ __forceinline__ int w_key(int row) { return ((row >> 1) & 1) | ((row >> 3) & 6); }
+// (two rows' chunk slots): rows of one parity have eight keys.  With S = up
+// to 4 matrix tiles of 16 outputs side by side in a wave, tile i takes the
+// LDS rows 4 S (r / 4) + 4 i + r % 4 (r = 0..15), so that a lane's results
+// over the S tiles are 4 S consecutive outputs and a row of y is written in
+// long pieces (whole 128-byte lines for S = 4).
+template <int S>
+__device__ __forceinline__ int w_key(int row) {
+  return ((row >> 1) & 1) | ((row >> (S == 4 ? 3 : S == 2 ? 2 : 1)) & 6);
+}
 __device__ __forceinline__ int a_key(int row) { return (row >> 1) & 7; }
 
 // Descriptor of `bytes` bytes at address v (raw, no stride); wave-uniform.
-__device__ __forceinline__ u32x4 buffer_of(uint64_t v, uint32_t bytes) {
+__device__ __forceinline__ u32x4 buffer_of(const void* p, uint32_t bytes) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
   return u32x4{static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(v))),
                static_cast<uint32_t>(
                    __builtin_amdgcn_readfirstlane(static_cast<int>((v >> 32) & 0xffff))),
@@ -204,39 +179,45 @@ __device__ __forceinline__ u32x4 buffer_of(uint64_t v, uint32_t bytes) {
                0x00020000u};
 }
 // 16 (4) bytes per lane from descriptor r at off to LDS address
-// lds + 16 (4) lane.  The s_nop covers the wait states between a vector
-// write of the descriptor's scalars, or the write of m0, and the load.
+// lds + 16 (4) lane.  The s_nop is the wait state between the write of m0 and
+// the load; r is scalar arithmetic's, except before the first load of all
+// (settle()).
 __device__ __forceinline__ void load_lds16(u32x4 r, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds),
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds),
                "v"(off), "s"(r)
                : "memory");
 }
 __device__ __forceinline__ void load_lds4(u32x4 r, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds),
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds),
                "v"(off), "s"(r)
                : "memory");
 }
+// The wait states between a vector write of a scalar and a load that uses it.
+__device__ __forceinline__ void settle() { asm volatile("s_nop 7" ::: "memory"); }
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
       (const __attribute__((address_space(3))) void*)p));
 }
 
-// Sixteen consecutive outputs n .. n+15 of a row.
-__device__ __forceinline__ void store16(float* row, int n, int N, const floatx4 (&v)[4]) {
+// 4 S consecutive outputs from n on of a row.
+template <int S>
+__device__ __forceinline__ void store_outputs(float* row, int n, int N, const floatx4 (&v)[S]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) store4(row, n + 4 * i, N, v[i]);
+  for (int i = 0; i < S; ++i) store4(row, n + 4 * i, N, v[i]);
 }
-__device__ __forceinline__ void store16(uint16_t* row, int n, int N, const floatx4 (&v)[4]) {
-  if (N % 8 == 0) {
+template <int S>
+__device__ __forceinline__ void store_outputs(uint16_t* row, int n, int N,
+                                              const floatx4 (&v)[S]) {
+  if (S > 1 && N % 8 == 0) {
 #pragma unroll
-    for (int i = 0; i < 4; i += 2)
+    for (int i = 0; i + 1 < S; i += 2)
       if (n + 4 * i < N)
         *reinterpret_cast<u32x4*>(row + n + 4 * i) =
             u32x4{pack_bf16x2(v[i][0], v[i][1]), pack_bf16x2(v[i][2], v[i][3]),
                   pack_bf16x2(v[i + 1][0], v[i + 1][1]), pack_bf16x2(v[i + 1][2], v[i + 1][3])};
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) store4(row, n + 4 * i, N, v[i]);
+    for (int i = 0; i < S; ++i) store4(row, n + 4 * i, N, v[i]);
   }
 }
 
@@ -257,23 +238,33 @@ __device__ __forceinline__ void tile_of(int id, int n_tiles, int m_tiles, int& n
   mt = r / width;
 }
 
-template <int BN, int BM, int WN, int WM, int STAGES, typename YT>
-__global__ __launch_bounds__(BN / WN * (BM / WM) * kWave) void fp8_tile_kernel(Fp8Args p,
-                                                                               int n_tiles,
-                                                                               int m_tiles) {
+template <int BN, int BM, int WN, int WM, int KG, int STAGES, typename YT>
+__global__ __launch_bounds__(KG* BN / WN * (BM / WM) * kWave) void fp8_tile_kernel(Fp8Args p,
+                                                                                   int n_tiles,
+                                                                                   int m_tiles) {
   constexpr bool kExact = sizeof(YT) == 4;
-  constexpr int kWaves = BN / WN * (BM / WM);
-  constexpr int kRowsPerLoad = 8 * kWaves;      // 8 LDS rows per wave instruction
-  constexpr int kWLoads = BN / kRowsPerLoad, kALoads = BM / kRowsPerLoad;
-  static_assert(kWLoads == 4 && kALoads == 4 && kRowsPerLoad % 32 == 0, "four loads each");
-  static_assert(WN % 64 == 0 && kFp8Run % WN == 0 && WM % 16 == 0, "");
-  constexpr int kABase = BN * kFp8Run, kSBase = kABase + BM * kFp8Run;
-  constexpr int kSwWave = BM / kWave;           // the wave that loads the weight scales
-  constexpr int kStage = kSBase + kWaves * kWave * 4;
+  constexpr int G = BN / WN * (BM / WM);        // waves of a group
+  constexpr int TI = WN / 16, TJ = WM / 16;     // a wave's matrix tiles
+  constexpr int S = TI < 4 ? TI : 4;            // of them side by side
+  constexpr int kRowsPerLoad = 8 * G;           // 8 LDS rows per wave instruction
+  constexpr int kARows = (BM + kRowsPerLoad - 1) / kRowsPerLoad * kRowsPerLoad;
+  constexpr int kWLoads = BN / kRowsPerLoad, kALoads = kARows / kRowsPerLoad;
+  static_assert(BN % kRowsPerLoad == 0 && TI % S == 0 && S != 3, "");
+  static_assert(BN <= kFp8Run ? kFp8Run % BN == 0 : BN % kFp8Run == 0, "");
+  static_assert(kFp8Run % WN == 0 && WM % 16 == 0, "");
+  // scales: 64 to a slot; first the rows', then one per 128 outputs
+  constexpr int kRowSlots = (BM + kWave - 1) / kWave, kBlocks = (BN + kFp8Run - 1) / kFp8Run;
+  constexpr int kSLoads = (kRowSlots + 1 + G - 1) / G, kSlots = kSLoads * G;
   constexpr int kAhead = STAGES - 1;            // runs in flight
-  constexpr int kLoads = kWLoads + kALoads + 1;   // of a wave per run
-  static_assert(kSwWave < kWaves && BN / kFp8Run <= kWave, "");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES][kStage];
+  constexpr int kLoads = kWLoads + kALoads + kSLoads;   // of a wave per run
+  static_assert((kAhead - 1) * kLoads < 64, "the counter of loads in flight");
+  // one array: the stages' w rows, their a rows, their scales, so that a
+  // stage is an immediate offset of the reads
+  constexpr int kWRun = BN * kFp8Run, kARun = kARows * kFp8Run, kSRun = kSlots * kWave * 4;
+  constexpr int kABase = STAGES * KG * kWRun, kSBase = kABase + STAGES * KG * kARun;
+  constexpr int kLds = kSBase + STAGES * KG * kSRun;
+  static_assert(kLds <= 160 * 1024 && (KG - 1) * G * TI * TJ * 1024 <= kLds, "");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
   int nt, mt;
   tile_of(blockIdx.x, n_tiles, m_tiles, nt, mt);
   Tile t;
@@ -283,245 +274,375 @@ __global__ __launch_bounds__(BN / WN * (BM / WM) * kWave) void fp8_tile_kernel(F
   t.count = __builtin_amdgcn_readfirstlane(t.count);
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int group = KG == 1 ? 0 : wave / G, gw = KG == 1 ? wave : wave % G;
   const int n0 = nt * BN;
   const int K = p.K, KB = p.KB;
 
-  // what this thread loads: LDS row lr + i kRowsPerLoad, chunk lane % 8
-  const int lr = 8 * wave + (lane >> 3);
-  const int ac = 16 * ((lane & 7) ^ a_key(lr));
-  auto wc = [&](int i) { return 16 * ((lane & 7) ^ w_key(lr + i * kRowsPerLoad)); };
-  uint32_t woff[kWLoads], aoff[kALoads];
+  // what this lane loads: LDS rows lr + i kRowsPerLoad, chunk lane % 8
+  const int lr = 8 * gw + (lane >> 3);
+  auto wc = [&](int i) { return 16 * ((lane & 7) ^ w_key<S>(lr + i * kRowsPerLoad)); };
+  auto ac = [&](int i) { return 16 * ((lane & 7) ^ a_key(lr + i * kRowsPerLoad)); };
+  uint32_t woff[kWLoads], aoff[kALoads], soff[kSLoads];
 #pragma unroll
   for (int i = 0; i < kWLoads; ++i) woff[i] = (lr + i * kRowsPerLoad) * K + wc(i);
   const uint8_t* abase = p.a;
-  const float* sabase = p.as;
-  uint32_t abytes, sabytes;
-  constexpr uint32_t kOut = 0x80000000u;
-  // the first waves load the row scales, wave kSwWave a scale per 128
-  // outputs, the others zeros (every wave counts the same loads)
-  uint32_t soff = kOut;
+  const float* asbase = p.as;
+  uint32_t abytes, asbytes;
   if (p.rows == nullptr) {
     abase += static_cast<size_t>(t.row0) * K;
-    sabase += static_cast<size_t>(t.row0) * KB;
+    asbase += static_cast<size_t>(t.row0) * KB;
     abytes = t.count * K;
-    sabytes = t.count * KB * 4;
+    asbytes = t.count * KB * 4;
 #pragma unroll
-    for (int i = 0; i < kALoads; ++i) aoff[i] = (lr + i * kRowsPerLoad) * K + ac;
-    if (wave < kSwWave) soff = threadIdx.x * KB * 4;
+    for (int i = 0; i < kALoads; ++i) aoff[i] = (lr + i * kRowsPerLoad) * K + ac(i);
   } else {
-    abytes = static_cast<uint32_t>(p.a_rows) * K;       // below 2^31 (host)
-    sabytes = static_cast<uint32_t>(p.a_rows) * KB * 4;
+    abytes = static_cast<uint32_t>(p.a_rows) * K;
+    asbytes = static_cast<uint32_t>(p.a_rows) * KB * 4;
 #pragma unroll
     for (int i = 0; i < kALoads; ++i) {
       const int r = lr + i * kRowsPerLoad;
       const int src = r < t.count ? source_row(p, t.row0 + r) : -1;
-      aoff[i] = src < 0 ? kOut : static_cast<uint32_t>(src) * K + ac;
-    }
-    if (static_cast<int>(threadIdx.x) < min(BM, t.count)) {
-      const int src = source_row(p, t.row0 + threadIdx.x);
-      if (src >= 0) soff = static_cast<uint32_t>(src) * KB * 4;
+      aoff[i] = src < 0 ? kOut : static_cast<uint32_t>(src) * K + ac(i);
     }
   }
   const uint8_t* wbase = p.w + (static_cast<size_t>(t.e) * p.N + n0) * K;
   const uint32_t wbytes = min(BN, p.N - n0) * K;
-  if (wave == kSwWave) {
-    const int blocks = fp8_runs(p.N), b0 = n0 / kFp8Run;
-    sabase = p.ws + (static_cast<size_t>(t.e) * blocks + b0) * KB;
-    sabytes = min(BN / kFp8Run, blocks - b0) * KB * 4;
-    soff = lane < BN / kFp8Run ? lane * KB * 4 : kOut;
-  }
+  const int blocks = fp8_runs(p.N), b0 = n0 / kFp8Run;
+  const float* wsbase = p.ws + (static_cast<size_t>(t.e) * blocks + b0) * KB;
+  const uint32_t wsbytes = min(kBlocks, blocks - b0) * KB * 4;
   const int tail = K % kFp8Run;      // inputs of the last run, 0: all 128
 
-  const uint32_t lds_base = __builtin_amdgcn_readfirstlane(lds_address(lds)) + wave * 1024;
-  const uint32_t lds_scales = lds_base - wave * 1024 + kSBase + wave * 256;
-  // the next run to load: its bases and the bytes behind them
-  uint64_t wp = reinterpret_cast<uint64_t>(wbase), ap = reinterpret_cast<uint64_t>(abase),
-           sp = reinterpret_cast<uint64_t>(sabase);
-  uint32_t wleft = wbytes, aleft = abytes, sleft = sabytes;
+  const uint32_t lds_base = __builtin_amdgcn_readfirstlane(lds_address(lds));
+  const uint32_t lds_w = lds_base + group * kWRun + gw * 1024,
+                 lds_a = lds_base + kABase + group * kARun + gw * 1024,
+                 lds_s = lds_base + kSBase + group * kSRun + gw * (kWave * 4);
+  // descriptors of the group's next run to load: its bases and the bytes
+  // behind them
+  auto first = [&](const void* base, uint32_t bytes, int by) {
+    return buffer_of(static_cast<const uint8_t*>(base) + group * by,
+                     group < KB ? bytes - group * by : 0);
+  };
+  u32x4 dw = first(wbase, wbytes, kFp8Run), da = first(abase, abytes, kFp8Run), ds[kSLoads];
+#pragma unroll
+  for (int u = 0; u < kSLoads; ++u) {
+    const int slot = gw + u * G;
+    const bool of_rows = slot < kRowSlots;
+    ds[u] = of_rows ? first(asbase, asbytes, 4) : first(wsbase, wsbytes, 4);
+    soff[u] = of_rows ? (slot * kWave + lane) * KB * 4 : lane * KB * 4;
+    if (slot > kRowSlots || (!of_rows && lane >= kBlocks)) soff[u] = kOut;
+    if (of_rows && p.rows != nullptr) {
+      const int r = slot * kWave + lane;
+      const int src = r < min(BM, t.count) ? source_row(p, t.row0 + r) : -1;
+      soff[u] = src < 0 ? kOut : static_cast<uint32_t>(src) * KB * 4;
+    }
+  }
   auto cut = [&]() {   // the last run: inputs from K on read as zeros
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      woff[i] = wc(i) >= tail ? kOut : woff[i];
-      aoff[i] = ac >= tail ? kOut : aoff[i];
+    for (int i = 0; i < kWLoads; ++i) woff[i] = wc(i) >= tail ? kOut : woff[i];
+#pragma unroll
+    for (int i = 0; i < kALoads; ++i) aoff[i] = ac(i) >= tail ? kOut : aoff[i];
+  };
+  // Load n (0 .. kLoads - 1) of the next run into `stage`.  The last load
+  // through a descriptor moves it on to the group's run after that; where
+  // there is none (keep == 0) it is left empty, and the loads through it
+  // write zeros and read nothing.
+  uint32_t keep = 0;
+  auto move = [&](u32x4& d, uint32_t by) {
+    const uint64_t v = (static_cast<uint64_t>(d[1]) << 32 | d[0]) + by;
+    d[0] = static_cast<uint32_t>(v);
+    d[1] = static_cast<uint32_t>(v >> 32);
+    d[2] = (d[2] - by) & keep;
+  };
+  auto load = [&](int n, int stage) {
+    if (n < kWLoads) {
+      load_lds16(dw, woff[n], lds_w + stage * (KG * kWRun) + n * (kRowsPerLoad * kFp8Run));
+      if (n == kWLoads - 1) move(dw, KG * kFp8Run);
+    } else if (n < kWLoads + kALoads) {
+      const int i = n - kWLoads;
+      load_lds16(da, aoff[i], lds_a + stage * (KG * kARun) + i * (kRowsPerLoad * kFp8Run));
+      if (i == kALoads - 1) move(da, KG * kFp8Run);
+    } else {
+      const int u = n - kWLoads - kALoads;
+      load_lds4(ds[u], soff[u], lds_s + stage * (KG * kSRun) + u * (G * kWave * 4));
+      move(ds[u], KG * 4);
     }
   };
-  // load n (0 .. kLoads - 1) of the next run into `stage`
-  auto load = [&](int n, int stage) {
-    const uint32_t at = stage * kStage;
-    if (n < kWLoads)
-      load_lds16(buffer_of(wp, wleft), woff[n],
-                 lds_base + at + n * (kRowsPerLoad * kFp8Run));
-    else if (n < kWLoads + kALoads)
-      load_lds16(buffer_of(ap, aleft), aoff[n - kWLoads],
-                 lds_base + at + kABase + (n - kWLoads) * (kRowsPerLoad * kFp8Run));
-    else
-      load_lds4(buffer_of(sp, sleft), soff, lds_scales + at);
-  };
-  // moves on to run kb; from KB on the descriptors are empty and the loads
-  // only write zeros
-  auto advance = [&](int kb) {
-    wp += kFp8Run;
-    ap += kFp8Run;
-    sp += 4;
-    wleft = kb < KB ? wleft - kFp8Run : 0;
-    aleft = kb < KB ? aleft - kFp8Run : 0;
-    sleft = kb < KB ? sleft - 4 : 0;
+  // before the loads of step s's run
+  auto ready = [&](int s) {
+    const int kb = s * KG + group;
     if (tail != 0 && kb == KB - 1) cut();
+    keep = kb + KG < KB ? ~0u : 0u;
   };
 
-  const int wn = (wave % (BN / WN)) * WN, wm = (wave / (BN / WN)) * WM;
+  const int wn = (gw % (BN / WN)) * WN, wm = (gw / (BN / WN)) * WM;
   const int g = lane >> 4, c = lane & 15;
-  floatx4 acc[WN / 16][WM / 16];
+  floatx4 acc[TI][TJ];
 #pragma unroll
-  for (int i = 0; i < WN / 16; ++i)
+  for (int i = 0; i < TI; ++i)
 #pragma unroll
-    for (int j = 0; j < WM / 16; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < TJ; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // fragment of LDS row `row` (16-byte chunks 2 g and 2 g + 1)
-  auto fragment = [&](const uint8_t* base, int row, int key) {
-    const u32x4 lo = *reinterpret_cast<const u32x4*>(base + row * kFp8Run + 16 * ((2 * g) ^ key));
-    const u32x4 hi =
-        *reinterpret_cast<const u32x4*>(base + row * kFp8Run + 16 * ((2 * g + 1) ^ key));
-    return i32x8{static_cast<int>(lo[0]), static_cast<int>(lo[1]), static_cast<int>(lo[2]),
-                 static_cast<int>(lo[3]), static_cast<int>(hi[0]), static_cast<int>(hi[1]),
-                 static_cast<int>(hi[2]), static_cast<int>(hi[3])};
+  // fragments: 16-byte chunks 2 g and 2 g + 1 of an LDS row.  All rows a
+  // lane reads have one key, so a fragment is two addresses and an offset.
+  const int wrow = wn + 4 * S * (c >> 2) + (c & 3), arow = wm + c;
+  const uint8_t* wl = lds + group * kWRun + wrow * kFp8Run;
+  const uint8_t* al = lds + kABase + group * kARun + arow * kFp8Run;
+  const uint8_t *wlo = wl + 16 * ((2 * g) ^ w_key<S>(wrow)),
+                *whi = wl + 16 * ((2 * g + 1) ^ w_key<S>(wrow));
+  const uint8_t *alo = al + 16 * ((2 * g) ^ a_key(arow)),
+                *ahi = al + 16 * ((2 * g + 1) ^ a_key(arow));
+  auto w_fragment = [&](int stage, int i) {   // tile i: rows wrow + 16 S (i / S) + 4 (i % S)
+    const int off = stage * (KG * kWRun) + (16 * S * (i / S) + 4 * (i % S)) * kFp8Run;
+    return join(*reinterpret_cast<const u32x4*>(wlo + off),
+                *reinterpret_cast<const u32x4*>(whi + off));
   };
-
-  constexpr int TI = WN / 16, TJ = WM / 16;
-  auto w_fragment = [&](const uint8_t* st, int i) {
-    const int row = wn + 64 * (i / 4) + 16 * (c >> 2) + 4 * (i % 4) + (c & 3);
-    return fragment(st, row, w_key(row));
+  auto a_fragment = [&](int stage, int j) {
+    const int off = stage * (KG * kARun) + 16 * j * kFp8Run;
+    return join(*reinterpret_cast<const u32x4*>(alo + off),
+                *reinterpret_cast<const u32x4*>(ahi + off));
   };
-  if (tail != 0 && KB == 1) cut();
-  for (int kb = 0; kb < kAhead; ++kb) {
-#pragma unroll
-    for (int n = 0; n < kLoads; ++n) load(n, kb);
-    advance(kb + 1);
-  }
-  // Step kb: the products of run kb - 1 that are left (its last two weight
-  // rows of tiles), under which the first operands of run kb are read, then
-  // run kb up to its own last two rows.  All reads of a run are thus done
-  // before the barrier that ends the step it began in, the loads of a run
-  // have that whole step to arrive, and the matrix pipe does not wait for
-  // LDS behind the barrier.
-  constexpr int kRows = 2, kRest = kRows * TJ, kProducts = TI * TJ;
-  // the scaled addition of a product comes kLag products after its issue: by
-  // then the matrix pipe has finished it and works on the later ones
-  constexpr int kLag = kExact ? 1 : 3;
-  // a load per kEvery products: issued in one go the loads fill the address
-  // queue and hold up the wave's matrix instructions
-  constexpr int kEvery = kProducts >= 2 * kLoads ? 2 : 1;
-  static_assert(kProducts >= kEvery * kLoads && TI % 4 == 0, "every load has a place");
-  i32x8 fa[TJ], fw[4];       // row i of weight tiles in fw[i % 4]
-  float s_old[TJ], s[TJ];
-#pragma unroll
-  for (int j = 0; j < TJ; ++j) {
-    fa[j] = i32x8{};
-    s[j] = 0.0f;
-  }
-  fw[2] = fw[3] = i32x8{};
-  int stage = 0;
-  floatx4 P[kLag + 1];
-  // product n of a step: the remaining rows column by column, so that each
-  // column's fa is free for the next run early, then the rows in order
-  auto row_of = [](int n) { return n < kRest ? TI - kRows + n % kRows : (n - kRest) / TJ; };
-  auto col_of = [](int n) { return n < kRest ? n / kRows : (n - kRest) % TJ; };
-  auto add = [&](int n) {
-    const int i = row_of(n), j = col_of(n);
-    const float f = n < kRest ? s_old[j] : s[j];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(f, P[n % (kLag + 1)][r], acc[i][j][r]);
-    asm volatile("" : "+v"(acc[i][j]));   // here, not at the end of the step
+  const float* sc = reinterpret_cast<const float*>(lds + kSBase + group * kSRun);
+  auto row_scale = [&](int stage, int j) { return sc[stage * (KG * kSRun / 4) + arow + 16 * j]; };
+  auto weight_scale = [&](int stage) {
+    return sc[stage * (KG * kSRun / 4) + kRowSlots * kWave + wn / kFp8Run];
   };
-  for (int kb = 0; kb < KB; ++kb) {
-    // this wave's loads of run kb have arrived (later runs' may still be in
-    // flight) and its reads of run kb - 1 are done; after the barrier that
-    // holds for every wave
+  // this wave's loads of the step's run have arrived (later ones may still be
+  // in flight) and its reads of the step before are done; after the barrier
+  // that holds for every wave.  A group of one wave loads for itself.
+  auto arrive = [&]() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((kAhead - 1) * kLoads) : "memory");
-    __builtin_amdgcn_s_barrier();
+    if constexpr (G > 1) __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    const uint8_t* st = lds[stage];
-    const int next = stage == 0 ? STAGES - 1 : stage - 1;
-    stage = stage + 1 == STAGES ? 0 : stage + 1;
-    const float* sc = reinterpret_cast<const float*>(st + kSBase);
-    const float swk = sc[BM + wn / kFp8Run];
+  };
+
+  asm volatile("" : "+s"(dw), "+s"(da));
+#pragma unroll
+  for (int u = 0; u < kSLoads; ++u) asm volatile("" : "+s"(ds[u]));
+  settle();
+  for (int s = 0; s < kAhead; ++s) {
+    ready(s);
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) load(n, s);
+  }
+  const int steps = (KB + KG - 1) / KG;
+  auto all_steps = [&](auto step) {
+    for (int s = 0; s < steps; s += STAGES) {
+      step(s, std::integral_constant<int, 0>{});
+      if (s + 1 < steps) step(s + 1, std::integral_constant<int, 1 % STAGES>{});
+      if constexpr (STAGES > 2)
+        if (s + 2 < steps) step(s + 2, std::integral_constant<int, 2 % STAGES>{});
+      if constexpr (STAGES > 3)
+        if (s + 3 < steps) step(s + 3, std::integral_constant<int, 3 % STAGES>{});
+      if constexpr (STAGES > 4)
+        if (s + 4 < steps) step(s + 4, std::integral_constant<int, 4 % STAGES>{});
+      static_assert(STAGES >= 2 && STAGES <= 5, "");
+    }
+  };
+
+  constexpr int kProducts = TI * TJ;
+  if constexpr (TI < 4) {
+    all_steps([&](int s, auto at) {
+      constexpr int stage = decltype(at)::value, next = (stage + kAhead) % STAGES;
+      arrive();
+      i32x8 fw[TI], fa[TJ];
+      float f[TJ];
+#pragma unroll
+      for (int i = 0; i < TI; ++i) fw[i] = w_fragment(stage, i);
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) fa[j] = a_fragment(stage, j);
+      const float swk = weight_scale(stage);
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) f[j] = row_scale(stage, j) * swk;
+      ready(s + kAhead);
+#pragma unroll
+      for (int n = 0; n < kLoads; ++n) load(n, next);
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+#pragma unroll
+        for (int i = 0; i < TI; ++i) {
+          const floatx4 P = mfma_run<kExact>(fw[i], fa[j]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(f[j], P[r], acc[i][j][r]);
+        }
+    });
+  } else {
+    // Step s: the products of the run before that are left (its last two
+    // rows of weight tiles), under which the first operands of this run are
+    // read, then this run up to its own last two rows.  All reads of a run
+    // are thus done before the barrier that ends the step it began in, the
+    // loads of a run have that whole step to arrive, and the matrix pipe
+    // does not wait for LDS behind the barrier.
+    constexpr int kRows = 2, kRest = kRows * TJ;
+    // the scaled addition of a product comes kLag products after its issue:
+    // by then the matrix pipe has finished it and works on the later ones
+    constexpr int kLag = kExact ? 1 : 3;
+    constexpr int kPer = (kLoads + kProducts - 1) / kProducts;
+    i32x8 fa[TJ], fw[4];       // row i of weight tiles in fw[i % 4]
+    float f_old[TJ], f[TJ];
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
-      s_old[j] = s[j];
-      s[j] = sc[wm + 16 * j + c];
+      fa[j] = i32x8{};
+      f[j] = 0.0f;
     }
-#pragma unroll
-    for (int n = 0; n < kProducts; ++n) {
+    fw[2] = fw[3] = i32x8{};
+    floatx4 P[kLag + 1];
+    // product n of a step: the remaining rows column by column, so that each
+    // column's fa is free for this run early, then the rows in order
+    auto row_of = [](int n) { return n < kRest ? TI - kRows + n % kRows : (n - kRest) / TJ; };
+    auto col_of = [](int n) { return n < kRest ? n / kRows : (n - kRest) % TJ; };
+    auto add = [&](int n) {
       const int i = row_of(n), j = col_of(n);
-      if (n < 2) fw[n] = w_fragment(st, n);
-      if (n >= kRest && j == 0) fw[(i + 2) % 4] = w_fragment(st, i + 2);
-      P[n % (kLag + 1)] = mfma_run<kExact>(fw[i % 4], fa[j]);
-      if (n < kRest && n % kRows == kRows - 1) {
-        const int row = wm + 16 * j + c;
-        fa[j] = fragment(st + kABase, row, a_key(row));
-      }
-      if (n == kRest) {
+      const float by = n < kRest ? f_old[j] : f[j];
 #pragma unroll
-        for (int u = 0; u < TJ; ++u) s[u] *= swk;
+      for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(by, P[n % (kLag + 1)][r], acc[i][j][r]);
+      asm volatile("" : "+v"(acc[i][j]));   // here, not at the end of the step
+    };
+    all_steps([&](int s, auto at) {
+      constexpr int stage = decltype(at)::value, next = (stage + kAhead) % STAGES;
+      arrive();
+      ready(s + kAhead);
+      const float swk = weight_scale(stage);
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        f_old[j] = f[j];
+        f[j] = row_scale(stage, j);
       }
-      if (n % kEvery == kEvery - 1 && n / kEvery < kLoads) load(n / kEvery, next);
-      if constexpr (!kExact) __builtin_amdgcn_sched_barrier(0);
-      if (n >= kLag) add(n - kLag);
-      if constexpr (!kExact) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int n = 0; n < kProducts; ++n) {
+        const int i = row_of(n), j = col_of(n);
+        if (n < 2) fw[n] = w_fragment(stage, n);
+        if (n >= kRest && j == 0) fw[(i + 2) % 4] = w_fragment(stage, i + 2);
+        P[n % (kLag + 1)] = mfma_run<kExact>(fw[i % 4], fa[j]);
+        if (n < kRest && n % kRows == kRows - 1) fa[j] = a_fragment(stage, j);
+        if (n == kRest) {
+#pragma unroll
+          for (int u = 0; u < TJ; ++u) f[u] *= swk;
+        }
+        // the next run's loads a few per product: issued in one go they fill
+        // the address queue and hold up the wave's matrix instructions
+#pragma unroll
+        for (int u = n * kPer; u < (n + 1) * kPer && u < kLoads; ++u) load(u, next);
+        if constexpr (!kExact) __builtin_amdgcn_sched_barrier(0);
+        if (n >= kLag) add(n - kLag);
+        if constexpr (!kExact) __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int n = kProducts - kLag; n < kProducts; ++n) add(n);
+    });
+#pragma unroll
+    for (int n = 0; n < kRest; ++n) {
+      const int i = row_of(n), j = col_of(n);
+      const floatx4 D = mfma_run<kExact>(fw[i % 4], fa[j]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(f[j], D[r], acc[i][j][r]);
     }
-#pragma unroll
-    for (int n = kProducts - kLag; n < kProducts; ++n) add(n);
-    advance(kb + kAhead + 1);
-  }
-#pragma unroll
-  for (int n = 0; n < kRest; ++n) {
-    const int i = row_of(n), j = col_of(n);
-    const floatx4 D = mfma_run<kExact>(fw[i % 4], fa[j]);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(s[j], D[r], acc[i][j][r]);
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no load outlives its LDS
+  if constexpr (KG > 1) {   // the groups' sums, in order
+    __syncthreads();
+    floatx4* part = reinterpret_cast<floatx4*>(lds) + gw * (TI * TJ * kWave) + lane;
+    if (group > 0) {
 #pragma unroll
-  for (int j = 0; j < WM / 16; ++j) {
+      for (int n = 0; n < kProducts; ++n)
+        part[((group - 1) * G * kProducts + n) * kWave] = acc[n / TJ][n % TJ];
+    }
+    __syncthreads();
+    if (group > 0) return;
+    for (int u = 0; u < KG - 1; ++u)
+#pragma unroll
+      for (int n = 0; n < kProducts; ++n)
+        acc[n / TJ][n % TJ] += part[(u * G * kProducts + n) * kWave];
+  }
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) {
     const int m = wm + 16 * j + c;
     if (m >= t.count) continue;
+    const bool none = p.rows != nullptr && source_row(p, t.row0 + m) < 0;
     YT* row = static_cast<YT*>(p.y) + static_cast<size_t>(t.row0 + m) * p.N;
 #pragma unroll
-    for (int i = 0; i < WN / 16; i += 4) {
-      const floatx4 v[4] = {acc[i][j], acc[i + 1][j], acc[i + 2][j], acc[i + 3][j]};
-      store16(row, n0 + wn + 16 * i + 16 * g, p.N, v);
+    for (int i = 0; i < TI; i += S) {
+      floatx4 v[S];
+#pragma unroll
+      for (int u = 0; u < S; ++u) v[u] = none ? floatx4{0.0f, 0.0f, 0.0f, 0.0f} : acc[i + u][j];
+      store_outputs<S>(row, n0 + wn + 16 * i + 4 * S * g, p.N, v);
     }
   }
 }
 
-template <int BN, int BM, int WN, int WM, int STAGES, typename YT>
+// ---- choice of the tile -----------------------------------------------------------
+
+template <int BN, int BM, int WN, int WM, int KG, int STAGES, typename YT>
 hipError_t launch_tile(const Fp8Args& p, int live, hipStream_t stream) {
   const int n_tiles = (p.N + BN - 1) / BN;
+  // sum_e ceil(c_e / BM) <= (M + live (BM - 1)) / BM
   const int m_tiles = static_cast<int>((p.M + static_cast<int64_t>(live) * (BM - 1)) / BM);
-  fp8_tile_kernel<BN, BM, WN, WM, STAGES, YT>
-      <<<dim3(n_tiles * m_tiles), BN / WN * (BM / WM) * kWave, 0, stream>>>(p, n_tiles, m_tiles);
+  fp8_tile_kernel<BN, BM, WN, WM, KG, STAGES, YT>
+      <<<dim3(n_tiles * m_tiles), KG * BN / WN * (BM / WM) * kWave, 0, stream>>>(p, n_tiles,
+                                                                                 m_tiles);
   return hipGetLastError();
 }
 
-}  // namespace
+// The tiles, largest first, and what a run of 128 inputs costs a round of
+// 256 tiles (one per CU), in ns, measured at 256 and 512 tiles of 64 runs.
+// The estimate rounds x cost picks the tile: large ones do the most work per
+// time (256 x 256 bf16: 39 outputs per ns and CU, 128 x 64: 21, 64 x 16: 7),
+// small ones leave no CU idle where there are few outputs.
+struct TileCost {
+  int bn, bm, bf16_ns, f32_ns;
+};
+constexpr TileCost kTiles[] = {
+    {256, 256, 1700, 0}, {256, 128, 960, 0},  {128, 128, 620, 1100}, {128, 128, 0, 920},
+    {128, 64, 380, 640}, {64, 64, 270, 400},  {64, 32, 165, 190},    {64, 16, 143, 145},
+    {32, 16, 95, 97},
+};
 
-namespace {
+int pick_tile(const Fp8Args& p, int live, bool bf16) {
+  int best = 0;
+  double least = 0.0;
+  const double rows = static_cast<double>(p.M) / live;   // of an expert, on average
+  for (int i = 0; i < static_cast<int>(sizeof kTiles / sizeof kTiles[0]); ++i) {
+    const TileCost& c = kTiles[i];
+    const int ns = bf16 ? c.bf16_ns : c.f32_ns;
+    if (ns == 0) continue;
+    // an expert's last tile is half empty on average; dense rows are known
+    double m_tiles = rows / c.bm + 0.5;
+    if (m_tiles < 1.0) m_tiles = 1.0;
+    m_tiles = p.offsets == nullptr ? (p.M + c.bm - 1) / c.bm : live * m_tiles;
+    const double rounds = ceil(m_tiles * ((p.N + c.bn - 1) / c.bn) / 256.0);
+    // two workgroups share a CU: only worth it from two tiles per CU on
+    if (i == 3 && rounds < 2.0) continue;
+    if (least == 0.0 || rounds * ns < least) {
+      least = rounds * ns;
+      best = i;
+    }
+  }
+  return best;
+}
 
 template <typename YT>
 hipError_t launch_by_size(const Fp8Args& p, hipStream_t stream) {
-  // experts with rows; sum_e ceil(c_e / BM) <= (M + live (BM - 1)) / BM
-  const int live = p.offsets == nullptr ? 1 : (p.E < p.M ? p.E : p.M);
-  // the tiles' buffer offsets reach 2^31 bytes into a where rows are gathered
-  const bool reach = p.rows == nullptr || static_cast<int64_t>(p.a_rows) * p.K < (int64_t{1} << 31);
-  if (p.M > 64 * live && reach) {
-    if constexpr (sizeof(YT) == 2) {
-      if (p.M > 512 * live) return launch_tile<256, 256, 128, 64, 2, YT>(p, live, stream);
-    }
-    return launch_tile<128, 128, 64, 64, 4, YT>(p, live, stream);
+  constexpr bool kBf16 = sizeof(YT) == 2;
+  const int live = p.offsets == nullptr ? 1 : (p.E < p.M ? p.E : p.M);   // experts with rows
+  switch (pick_tile(p, live, kBf16)) {
+    case 0:
+      if constexpr (kBf16) return launch_tile<256, 256, 128, 64, 1, 2, YT>(p, live, stream);
+    case 1:
+      if constexpr (kBf16) return launch_tile<256, 128, 64, 64, 1, 3, YT>(p, live, stream);
+    case 3:
+      if constexpr (!kBf16) return launch_tile<128, 128, 64, 64, 1, 2, YT>(p, live, stream);
+    case 2:
+      return launch_tile<128, 128, 64, 64, 1, 4, YT>(p, live, stream);
+    case 4:
+      return launch_tile<128, 64, 64, 32, 2, 3, YT>(p, live, stream);
+    case 5:
+      return launch_tile<64, 64, 64, 32, 2, 4, YT>(p, live, stream);
+    case 6:
+      return launch_tile<64, 32, 64, 32, 4, 3, YT>(p, live, stream);
+    case 7:
+      return launch_tile<64, 16, 64, 16, 4, 3, YT>(p, live, stream);
+    default:
+      return launch_tile<32, 16, 32, 16, 8, 3, YT>(p, live, stream);
   }
-  const dim3 grid((p.N + 15) / 16, (p.M + live * 15) / 16);
-  fp8_stream_kernel<YT><<<grid, 512, 0, stream>>>(p);
-  return hipGetLastError();
 }
 
 }  // namespace

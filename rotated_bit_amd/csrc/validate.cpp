@@ -476,6 +476,8 @@ harp_status validate_fp8_gemm_grouped(const harp_fp8_weight* W, const void* a,
   if (bad_dtype(y_dt)) return HARP_ERR_DTYPE;
   HARP_TRY(check_m(M));
   if (a_rows < 0 || a_rows > HARP_MAX_M) return HARP_ERR_SHAPE;
+  if (rows != nullptr && static_cast<int64_t>(a_rows) * W->K > int64_t{kFp8MaxGather})
+    return HARP_ERR_UNSUPPORTED;
   if (M > 0 && (a_rows < 1 || (rows == nullptr && a_rows < M))) return HARP_ERR_SHAPE;
   HARP_TRY(check_data(a, M));
   HARP_TRY(check_data(a_scale, M));

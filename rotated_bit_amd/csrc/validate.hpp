@@ -159,7 +159,8 @@ harp_status validate_chain(const harp_chain_layer* layers, int32_t n_layers, con
                            int x_dt, int y_dt, int32_t M, const void* workspace,
                            size_t ws_bytes);
 
-// 8-bit operators.
+// 8-bit operators.  Rows of a read by index are addressed with 32 bits.
+constexpr uint32_t kFp8MaxGather = 0xffffff00u;   // bytes of a
 harp_status check_fp8_weight(const harp_fp8_weight* W);
 // fp8: the checks of harp_rmsnorm_fp8 (y holds the codes, y_dt is not read);
 // otherwise those of harp_rmsnorm (q_scale is not read).

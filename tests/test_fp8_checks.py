@@ -109,6 +109,11 @@ def test_product_other_checks():
     assert grouped(a_rows=0) == L.HARP_ERR_SHAPE
     assert grouped(a_rows=3, M=4) == L.HARP_ERR_SHAPE          # no rows: one a row per y row
     assert grouped(a_rows=0, off=0, M=0) == L.HARP_OK
+    # gathered rows are addressed with 32 bits
+    wide = fw(K=131072)
+    assert grouped(W=wide, a_rows=32768, rows=FAKE, M=0) == L.HARP_ERR_UNSUPPORTED
+    assert grouped(W=wide, a_rows=32767, rows=FAKE, M=0) == L.HARP_OK
+    assert grouped(W=wide, a_rows=65536, M=0) == L.HARP_OK
 
 
 def test_binding_rejects_tensors():
