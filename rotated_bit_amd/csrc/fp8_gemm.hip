@@ -592,7 +592,7 @@ struct TileCost {
 };
 constexpr TileCost kTiles[] = {
     {256, 256, 1700, 0}, {256, 128, 960, 0},  {128, 128, 620, 1100}, {128, 128, 0, 920},
-    {128, 64, 380, 640}, {64, 64, 270, 400},  {64, 32, 165, 190},    {64, 16, 143, 145},
+    {128, 64, 380, 640}, {64, 64, 270, 0},  {64, 32, 165, 190},    {64, 16, 143, 145},
     {32, 16, 95, 97},
 };
 
@@ -635,7 +635,7 @@ hipError_t launch_by_size(const Fp8Args& p, hipStream_t stream) {
     case 4:
       return launch_tile<128, 64, 64, 32, 2, 3, YT>(p, live, stream);
     case 5:
-      return launch_tile<64, 64, 64, 32, 2, 4, YT>(p, live, stream);
+      if constexpr (kBf16) return launch_tile<64, 64, 64, 32, 2, 4, YT>(p, live, stream);
     case 6:
       return launch_tile<64, 32, 64, 32, 4, 3, YT>(p, live, stream);
     case 7:

@@ -223,7 +223,9 @@ SHAPES = [(1, 1, 16), (1, 16, 128), (1, 4096, 4096), (2, 17, 144), (3, 100, 112)
           (16, 1030, 4096), (17, 130, 400), (33, 96, 1040), (48, 2048, 2048), (64, 257, 1024),
           (65, 384, 1040), (100, 1000, 272), (128, 256, 2048), (129, 511, 144), (200, 1100, 1536),
           (256, 512, 512), (257, 640, 656), (300, 512, 4096), (513, 1153, 640),
-          (1024, 2304, 1152), (1500, 900, 16), (2100, 2050, 400)]
+          (1024, 2304, 1152), (1500, 900, 16), (2100, 2050, 400), (33, 5458, 400),
+          (17, 4162, 1040), (65, 5455, 272), (257, 3587, 656), (1000, 4001, 1040),
+          (1000, 4635, 144), (1500, 5391, 272), (700, 16400, 144), (50, 30000, 144)]
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
@@ -271,6 +273,8 @@ GROUPS = [
     ([0, 300, 0, 1, 129, 0, 0], 384, 656, True), ([128, 128, 257], 300, 512, False),
     ([5] * 70, 48, 160, True), ([0] * 130 + [3] + [0] * 70 + [9], 33, 144, True),
     ([700, 1, 2, 900], 260, 256, True), ([256] * 4, 512, 384, False),
+    ([700, 0, 900, 500], 5001, 272, True), ([100, 300, 0, 20] * 3, 2100, 144, False),
+    ([2500, 2, 3000], 4100, 144, True),
 ]
 
 
