@@ -112,6 +112,21 @@ __device__ __forceinline__ floatx4 mfma_run(i32x8 w, i32x8 a) {
     return d;
   }
 }
+// Two exact sums in turn: each of a sum's four instructions waits for the
+// one before it.
+__device__ __forceinline__ void mfma_run_pair(i32x8 w0, i32x8 a0, i32x8 w1, i32x8 a1,
+                                              floatx4& d0, floatx4& d1) {
+  d0 = d1 = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    d0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_bf16(w0[2 * i], w0[2 * i + 1]),
+                                                 codes_bf16(a0[2 * i], a0[2 * i + 1]), d0, 0, 0,
+                                                 0);
+    d1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_bf16(w1[2 * i], w1[2 * i + 1]),
+                                                 codes_bf16(a1[2 * i], a1[2 * i + 1]), d1, 0, 0,
+                                                 0);
+  }
+}
 
 // Outputs n .. n+3 of a row of N (one store where rows keep its alignment).
 __device__ __forceinline__ void store4(float* row, int n, int N, floatx4 v) {
@@ -474,8 +489,9 @@ __global__ __launch_bounds__(KG* BN / WN * (BM / WM) * kWave) void fp8_tile_kern
     // does not wait for LDS behind the barrier.
     constexpr int kRows = 2, kRest = kRows * TJ;
     // the scaled addition of a product comes kLag products after its issue:
-    // by then the matrix pipe has finished it and works on the later ones
-    constexpr int kLag = kExact ? 1 : 3;
+    // by then the matrix pipe has finished it and works on the later ones.
+    // Exact products are issued, and added, in pairs.
+    constexpr int kLag = kExact ? 2 : 3;
     constexpr int kPer = (kLoads + kProducts - 1) / kProducts;
     i32x8 fa[TJ], fw[4];       // row i of weight tiles in fw[i % 4]
     float f_old[TJ], f[TJ];
@@ -485,7 +501,7 @@ __global__ __launch_bounds__(KG* BN / WN * (BM / WM) * kWave) void fp8_tile_kern
       f[j] = 0.0f;
     }
     fw[2] = fw[3] = i32x8{};
-    floatx4 P[kLag + 1];
+    floatx4 P[4];
     // product n of a step: the remaining rows column by column, so that each
     // column's fa is free for this run early, then the rows in order
     auto row_of = [](int n) { return n < kRest ? TI - kRows + n % kRows : (n - kRest) / TJ; };
@@ -494,7 +510,7 @@ __global__ __launch_bounds__(KG* BN / WN * (BM / WM) * kWave) void fp8_tile_kern
       const int i = row_of(n), j = col_of(n);
       const float by = n < kRest ? f_old[j] : f[j];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(by, P[n % (kLag + 1)][r], acc[i][j][r]);
+      for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(by, P[n % 4][r], acc[i][j][r]);
       asm volatile("" : "+v"(acc[i][j]));   // here, not at the end of the step
     };
     all_steps([&](int s, auto at) {
@@ -512,7 +528,12 @@ __global__ __launch_bounds__(KG* BN / WN * (BM / WM) * kWave) void fp8_tile_kern
         const int i = row_of(n), j = col_of(n);
         if (n < 2) fw[n] = w_fragment(stage, n);
         if (n >= kRest && j == 0) fw[(i + 2) % 4] = w_fragment(stage, i + 2);
-        P[n % (kLag + 1)] = mfma_run<kExact>(fw[i % 4], fa[j]);
+        if constexpr (!kExact) {
+          P[n % 4] = mfma_run<false>(fw[i % 4], fa[j]);
+        } else if (n % 2 == 0) {
+          mfma_run_pair(fw[i % 4], fa[j], fw[row_of(n + 1) % 4], fa[col_of(n + 1)], P[n % 4],
+                        P[n % 4 + 1]);
+        }
         if (n < kRest && n % kRows == kRows - 1) fa[j] = a_fragment(stage, j);
         if (n == kRest) {
 #pragma unroll
@@ -522,9 +543,9 @@ __global__ __launch_bounds__(KG* BN / WN * (BM / WM) * kWave) void fp8_tile_kern
         // the address queue and hold up the wave's matrix instructions
 #pragma unroll
         for (int u = n * kPer; u < (n + 1) * kPer && u < kLoads; ++u) load(u, next);
-        if constexpr (!kExact) __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_sched_barrier(0);
         if (n >= kLag) add(n - kLag);
-        if constexpr (!kExact) __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int n = kProducts - kLag; n < kProducts; ++n) add(n);
@@ -583,18 +604,19 @@ hipError_t launch_tile(const Fp8Args& p, int live, hipStream_t stream) {
 }
 
 // The tiles, largest first, and what a run of 128 inputs costs a round of
-// 256 tiles (one per CU), in ns, measured at 256 and 512 tiles of 64 runs.
-// The estimate rounds x cost picks the tile: large ones do the most work per
-// time (256 x 256 bf16: 39 outputs per ns and CU, 128 x 64: 21, 64 x 16: 7),
-// small ones leave no CU idle where there are few outputs.
+// 256 tiles (one per CU), in ns, measured from the second such round of 64
+// runs.  The estimate rounds x cost picks the tile: large ones do the most
+// work per time (256 x 256 bf16: 36 outputs per ns and CU, 128 x 64: 21,
+// 64 x 16: 7), small ones leave no CU idle where there are few outputs.
 struct TileCost {
-  int bn, bm, bf16_ns, f32_ns;
+  int bn, bm, bf16_ns, f32_ns;   // 0: not built
 };
 constexpr TileCost kTiles[] = {
-    {256, 256, 1700, 0}, {256, 128, 960, 0},  {128, 128, 620, 1100}, {128, 128, 0, 920},
-    {128, 64, 380, 640}, {64, 64, 270, 0},  {64, 32, 165, 190},    {64, 16, 143, 145},
-    {32, 16, 95, 97},
+    {256, 256, 1800, 0}, {256, 128, 970, 0},  {128, 128, 610, 0}, {128, 128, 0, 1020},
+    {128, 128, 0, 920},  {128, 64, 390, 690}, {64, 64, 280, 0},   {64, 32, 180, 245},
+    {64, 16, 143, 165},  {32, 16, 105, 110},
 };
+constexpr int kSharedCu = 4;   // two workgroups share a CU: from two tiles per CU on
 
 int pick_tile(const Fp8Args& p, int live, bool bf16) {
   int best = 0;
@@ -609,8 +631,7 @@ int pick_tile(const Fp8Args& p, int live, bool bf16) {
     if (m_tiles < 1.0) m_tiles = 1.0;
     m_tiles = p.offsets == nullptr ? (p.M + c.bm - 1) / c.bm : live * m_tiles;
     const double rounds = ceil(m_tiles * ((p.N + c.bn - 1) / c.bn) / 256.0);
-    // two workgroups share a CU: only worth it from two tiles per CU on
-    if (i == 3 && rounds < 2.0) continue;
+    if (i == kSharedCu && rounds < 2.0) continue;
     if (least == 0.0 || rounds * ns < least) {
       least = rounds * ns;
       best = i;
@@ -626,19 +647,27 @@ hipError_t launch_by_size(const Fp8Args& p, hipStream_t stream) {
   switch (pick_tile(p, live, kBf16)) {
     case 0:
       if constexpr (kBf16) return launch_tile<256, 256, 128, 64, 1, 2, YT>(p, live, stream);
+      [[fallthrough]];
     case 1:
       if constexpr (kBf16) return launch_tile<256, 128, 64, 64, 1, 3, YT>(p, live, stream);
-    case 3:
-      if constexpr (!kBf16) return launch_tile<128, 128, 64, 64, 1, 2, YT>(p, live, stream);
+      [[fallthrough]];
     case 2:
-      return launch_tile<128, 128, 64, 64, 1, 4, YT>(p, live, stream);
+      if constexpr (kBf16) return launch_tile<128, 128, 64, 64, 1, 4, YT>(p, live, stream);
+      [[fallthrough]];
+    case 3:
+      if constexpr (!kBf16) return launch_tile<128, 128, 64, 64, 2, 2, YT>(p, live, stream);
+      [[fallthrough]];
     case 4:
-      return launch_tile<128, 64, 64, 32, 2, 3, YT>(p, live, stream);
+      if constexpr (!kBf16) return launch_tile<128, 128, 64, 64, 1, 2, YT>(p, live, stream);
+      [[fallthrough]];
     case 5:
-      if constexpr (kBf16) return launch_tile<64, 64, 64, 32, 2, 4, YT>(p, live, stream);
+      return launch_tile<128, 64, 64, 32, 2, 3, YT>(p, live, stream);
     case 6:
-      return launch_tile<64, 32, 64, 32, 4, 3, YT>(p, live, stream);
+      if constexpr (kBf16) return launch_tile<64, 64, 64, 32, 2, 4, YT>(p, live, stream);
+      [[fallthrough]];
     case 7:
+      return launch_tile<64, 32, 64, 32, 4, 3, YT>(p, live, stream);
+    case 8:
       return launch_tile<64, 16, 64, 16, 4, 3, YT>(p, live, stream);
     default:
       return launch_tile<32, 16, 32, 16, 8, 3, YT>(p, live, stream);
