@@ -595,7 +595,9 @@ __global__ __launch_bounds__(KG* BN / WN * (BM / WM) * kWave) void fp8_tile_kern
 template <int BN, int BM, int WN, int WM, int KG, int STAGES, typename YT>
 hipError_t launch_tile(const Fp8Args& p, int live, hipStream_t stream) {
   const int n_tiles = (p.N + BN - 1) / BN;
-  // sum_e ceil(c_e / BM) <= (M + live (BM - 1)) / BM
+  // sum_e ceil(c_e / BM) <= (M + live (BM - 1)) / BM.  With the tile picked
+  // below the threads stay under the 2^32 a launch may have (1.7e9 at most,
+  // for 40000 rows of 1024 experts with 262144 outputs).
   const int m_tiles = static_cast<int>((p.M + static_cast<int64_t>(live) * (BM - 1)) / BM);
   fp8_tile_kernel<BN, BM, WN, WM, KG, STAGES, YT>
       <<<dim3(n_tiles * m_tiles), KG * BN / WN * (BM / WM) * kWave, 0, stream>>>(p, n_tiles,

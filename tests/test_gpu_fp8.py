@@ -274,7 +274,11 @@ GROUPS = [
     ([5] * 70, 48, 160, True), ([0] * 130 + [3] + [0] * 70 + [9], 33, 144, True),
     ([700, 1, 2, 900], 260, 256, True), ([256] * 4, 512, 384, False),
     ([700, 0, 900, 500], 5001, 272, True), ([100, 300, 0, 20] * 3, 2100, 144, False),
-    ([2500, 2, 3000], 4100, 144, True),
+    ([2500, 2, 3000], 4100, 144, True), ([5, 0, 20], 4832, 400, True),
+    ([0, 200, 5, 60, 20, 1, 20, 1, 20], 3330, 144, True),
+    ([200, 5, 0, 100, 20, 1, 5, 0, 130], 3398, 272, True),
+    ([100, 5, 5, 0, 0, 100, 1, 0], 3734, 656, True),
+    ([5, 60, 100, 5, 20, 60, 0, 300, 0, 0, 20], 4887, 144, False),
 ]
 
 
@@ -319,6 +323,31 @@ def test_grouped_rows_out_of_range_are_zero(sizes):
     fine = torch.ones(M, dtype=torch.bool, device="cuda")
     fine[bad] = False
     assert torch.all((y[fine] != 0).any(1)) and torch.isfinite(y).all()
+
+
+@pytest.mark.parametrize("sizes,N", [([3, 2, 4], 40), ([30, 70, 90], 500), ([300, 1, 400], 2100)])
+def test_grouped_nan_stays_where_it_is(sizes, N):
+    # NaN codes and scales in rows nobody asks for, in one row of one expert
+    # and in another expert's weights
+    rng = np.random.default_rng(12)
+    M, K, a_rows = sum(sizes), 272, 50
+    W, wq, ws = weight(rng, N, K, 3)
+    a, sa, aq, as_ = rows_of(rng, a_rows, K)
+    rows = rng.integers(0, 40, M)
+    off = np.concatenate([[0], np.cumsum(sizes)])
+    rows[0] = 60                                          # no such row: zeros, of a NaN weight too
+    rows[off[1]] = 45
+    a.view(torch.uint8)[40:] = 0x7f
+    sa[40:] = float("nan")
+    W.w.view(torch.uint8)[0, N // 2, 7] = 0xff
+    y = torch.empty((M, N), device="cuda")
+    lib().harp_fp8_gemm_grouped(W, a, sa, sizes_to_offsets(sizes), y,
+                                rows=torch.tensor(rows, dtype=torch.int32, device="cuda"))
+    want = np.zeros((M, N), dtype=bool)
+    want[1:off[1], N // 2] = True
+    want[off[1]] = True
+    assert np.array_equal(torch.isnan(y).cpu().numpy(), want)
+    assert torch.all(y[0] == 0)
 
 
 @pytest.mark.parametrize("M", [6, 90, 600])
