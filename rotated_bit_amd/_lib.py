@@ -433,21 +433,17 @@ def harp_quantize_pack(Wp, bits: int, qweight, scale, zero, stream=None) -> None
 
 # 8-bit operators.  Their tensors are checked here as well (device, type,
 # shape, contiguous rows): the C entry points see plain addresses.  A call
-# at decode sizes takes a few microseconds on the GPU, so the checks are one
-# expression per tensor, and only a tensor that fails one is looked at for
-# the message.
+# at decode sizes takes 2 to 6 us on the GPU and its launch 3 us on the host,
+# so the checks are one expression per tensor, only a tensor that fails one
+# is looked at for the message, and the handle of the current stream is read
+# without a Stream object around it (torch.cuda.current_stream(): 2.7 us).
 
 def _runs(n: int) -> int:
     return (n + 127) >> 7
 
 
-def _fine(t, shape, dtypes, index) -> bool:
-    return (t.shape == shape and t.dtype in dtypes and t.is_contiguous()
-            and t.get_device() == index)
-
-
 def _reject(name: str, t, shape, dtypes, index):
-    """Raises for a tensor that is not _fine."""
+    """Raises for a tensor that is not what its call needs."""
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype not in dtypes:
@@ -460,46 +456,38 @@ def _reject(name: str, t, shape, dtypes, index):
 
 
 def _expect(name: str, t, shape, dtypes, index):
-    if not _fine(t, shape, dtypes, index):
+    if not (t.shape == shape and t.dtype in dtypes and t.is_contiguous()
+            and t.get_device() == index):
         _reject(name, t, shape, dtypes, index)
 
 
-def _current_stream(index: int) -> int:
-    """Handle of the current stream of GPU `index`.  torch's accessor of the
-    handle alone takes 0.1 us; torch.cuda.current_stream() builds a Stream
-    object first (2.7 us, as much as the launch)."""
-    if _raw_stream is not None:
-        return _raw_stream(index)
-    return _torch().cuda.current_stream(index).cuda_stream
+def _accessors():
+    torch = _torch()
+    device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                     lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return (device, stream, {torch.float32: HARP_F32, torch.bfloat16: HARP_BF16},
+            (torch.float8_e4m3fn, torch.uint8), (torch.float32,), (torch.int32,))
 
 
-_raw_stream = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
+_current_device, _current_stream, _FLOATS, _CODES, _F32, _I32 = _accessors()
 
 
-def _call(where, f, index, stream, *args):
+def _call(where, f, index, stream, args):
     """f on the tensors' device (made current for the call) and stream."""
     if index < 0:
         raise ValueError(f"{where}: expected tensors on a GPU")
-    s = (_current_stream(index) if stream is None else stream if isinstance(stream, int)
-         else stream.cuda_stream)
-    cuda = _torch().cuda
-    if index == cuda.current_device():
-        status = f(*args, s)
+    if stream is None:
+        stream = _current_stream(index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if index == _current_device():
+        status = f(*args, stream)
     else:
-        with cuda.device(index):
-            status = f(*args, s)
+        with _torch().cuda.device(index):
+            status = f(*args, stream)
     if status != HARP_OK:
         _check(status, where)
-
-
-def _types():
-    torch = _torch()
-    f32 = (torch.float32,)
-    return ({torch.float32: HARP_F32, torch.bfloat16: HARP_BF16},
-            (torch.float8_e4m3fn, torch.uint8), f32, (torch.int32,))
-
-
-_FLOATS, _CODES, _F32, _I32 = _types()
 
 
 class FP8Weight:
@@ -512,86 +500,95 @@ class FP8Weight:
             raise ValueError("w: [N][K] or [experts][N][K]")
         self.experts = w.shape[0] if w.dim() == 3 else 1
         self.N, self.K = w.shape[-2:]
+        self.runs = _runs(self.K)
         self.index = w.get_device()
         _expect("w", w, w.shape, _CODES, self.index)
-        _expect("scale", scale, (*w.shape[:-2], _runs(self.N), _runs(self.K)), _F32, self.index)
+        _expect("scale", scale, (*w.shape[:-2], _runs(self.N), self.runs), _F32, self.index)
         self.w, self.scale = w, scale
         self.c = harp_fp8_weight(self.N, self.K, self.experts, w.data_ptr(), scale.data_ptr())
         self.ref = ctypes.byref(self.c)
 
 
 def _norm_inputs(x, weight, residual, residual_out):
-    """(M, D, device index, x's dtype, weight's dtype, residual addresses)."""
-    shape, index = x.shape, x.get_device()
+    """(M, D, x's device, its first six arguments of the C call)."""
+    shape, index, dtype = x.shape, x.get_device(), x.dtype
     if len(shape) != 2:
         raise ValueError("x: [M][D]")
-    _expect("x", x, shape, _FLOATS, index)
-    _expect("weight", weight, shape[1:], _FLOATS, index)
-    same = (x.dtype,)
+    if not (dtype in _FLOATS and x.is_contiguous()):
+        _reject("x", x, shape, _FLOATS, index)
+    M, D = shape
+    if not (weight.shape == (D,) and weight.dtype in _FLOATS and weight.is_contiguous()
+            and weight.get_device() == index):
+        _reject("weight", weight, (D,), _FLOATS, index)
     r = ro = None
     if residual is not None:
-        _expect("residual", residual, shape, same, index)
+        if not (residual.shape == shape and residual.dtype == dtype
+                and residual.is_contiguous() and residual.get_device() == index):
+            _reject("residual", residual, shape, (dtype,), index)
         r = residual.data_ptr()
     if residual_out is not None:
-        _expect("residual_out", residual_out, shape, same, index)
+        if not (residual_out.shape == shape and residual_out.dtype == dtype
+                and residual_out.is_contiguous() and residual_out.get_device() == index):
+            _reject("residual_out", residual_out, shape, (dtype,), index)
         ro = residual_out.data_ptr()
-    return shape[0], shape[1], index, _FLOATS[x.dtype], _FLOATS[weight.dtype], r, ro
+    return M, D, index, (x.data_ptr(), _FLOATS[dtype], r, ro, weight.data_ptr(),
+                         _FLOATS[weight.dtype])
 
 
 def harp_rmsnorm(x, weight, y, eps: float = 1e-6, residual=None, residual_out=None,
                  stream=None) -> None:
     """y = norm(x + residual) * weight for x [M][D], and residual_out = x + residual."""
-    M, D, index, xdt, wdt, r, ro = _norm_inputs(x, weight, residual, residual_out)
-    _expect("y", y, x.shape, _FLOATS, index)
-    _call("harp_rmsnorm", lib.harp_rmsnorm, index, stream, x.data_ptr(), xdt, r, ro,
-          weight.data_ptr(), wdt, eps, y.data_ptr(), _FLOATS[y.dtype], M, D)
+    M, D, index, args = _norm_inputs(x, weight, residual, residual_out)
+    _expect("y", y, (M, D), _FLOATS, index)
+    _call("harp_rmsnorm", lib.harp_rmsnorm, index, stream,
+          (*args, eps, y.data_ptr(), _FLOATS[y.dtype], M, D))
 
 
 def harp_rmsnorm_fp8(x, weight, q, q_scale, eps: float = 1e-6, residual=None, residual_out=None,
                      stream=None) -> None:
     """harp_rmsnorm with its output as codes q [M][D] and q_scale [M][ceil(D/128)]."""
-    M, D, index, xdt, wdt, r, ro = _norm_inputs(x, weight, residual, residual_out)
-    _expect("q", q, x.shape, _CODES, index)
-    _expect("q_scale", q_scale, (M, _runs(D)), _F32, index)
-    _call("harp_rmsnorm_fp8", lib.harp_rmsnorm_fp8, index, stream, x.data_ptr(), xdt, r, ro,
-          weight.data_ptr(), wdt, eps, q.data_ptr(), q_scale.data_ptr(), M, D)
+    M, D, index, args = _norm_inputs(x, weight, residual, residual_out)
+    _expect("q", q, (M, D), _CODES, index)
+    _expect("q_scale", q_scale, (M, (D + 127) >> 7), _F32, index)
+    _call("harp_rmsnorm_fp8", lib.harp_rmsnorm_fp8, index, stream,
+          (*args, eps, q.data_ptr(), q_scale.data_ptr(), M, D))
 
 
 def harp_silu_mul_fp8(gate_up, q, q_scale, stream=None) -> None:
     """Codes of silu(gate) * up for gate_up [M][2 D] (gates first)."""
     M, D = q.shape
     index = q.get_device()
-    _expect("q", q, q.shape, _CODES, index)
+    _expect("q", q, (M, D), _CODES, index)
     _expect("gate_up", gate_up, (M, 2 * D), _FLOATS, index)
-    _expect("q_scale", q_scale, (M, _runs(D)), _F32, index)
-    _call("harp_silu_mul_fp8", lib.harp_silu_mul_fp8, index, stream, gate_up.data_ptr(),
-          _FLOATS[gate_up.dtype], q.data_ptr(), q_scale.data_ptr(), M, D)
+    _expect("q_scale", q_scale, (M, (D + 127) >> 7), _F32, index)
+    _call("harp_silu_mul_fp8", lib.harp_silu_mul_fp8, index, stream,
+          (gate_up.data_ptr(), _FLOATS[gate_up.dtype], q.data_ptr(), q_scale.data_ptr(), M, D))
 
 
 def harp_fp8_gemm(W: FP8Weight, a, a_scale, y, stream=None) -> None:
     """y [M][N] = W a for codes a [M][K] with a_scale [M][ceil(K/128)]."""
     M, index = a.shape[0], W.index
     _expect("a", a, (M, W.K), _CODES, index)
-    _expect("a_scale", a_scale, (M, _runs(W.K)), _F32, index)
+    _expect("a_scale", a_scale, (M, W.runs), _F32, index)
     _expect("y", y, (M, W.N), _FLOATS, index)
-    _call("harp_fp8_gemm", lib.harp_fp8_gemm, index, stream, W.ref, a.data_ptr(),
-          a_scale.data_ptr(), y.data_ptr(), _FLOATS[y.dtype], M)
+    _call("harp_fp8_gemm", lib.harp_fp8_gemm, index, stream,
+          (W.ref, a.data_ptr(), a_scale.data_ptr(), y.data_ptr(), _FLOATS[y.dtype], M))
 
 
 def harp_fp8_gemm_grouped(W: FP8Weight, a, a_scale, offsets, y, rows=None, stream=None) -> None:
     """y[i] = W_e a[rows[i]] for offsets[e] <= i < offsets[e + 1] (int32 device tensors)."""
     a_rows, M, index = a.shape[0], y.shape[0], W.index
     _expect("a", a, (a_rows, W.K), _CODES, index)
-    _expect("a_scale", a_scale, (a_rows, _runs(W.K)), _F32, index)
+    _expect("a_scale", a_scale, (a_rows, W.runs), _F32, index)
     _expect("offsets", offsets, (W.experts + 1,), _I32, index)
     _expect("y", y, (M, W.N), _FLOATS, index)
     r = None
     if rows is not None:
         _expect("rows", rows, (M,), _I32, index)
         r = rows.data_ptr()
-    _call("harp_fp8_gemm_grouped", lib.harp_fp8_gemm_grouped, index, stream, W.ref,
-          a.data_ptr(), a_scale.data_ptr(), a_rows, r, offsets.data_ptr(), y.data_ptr(),
-          _FLOATS[y.dtype], M)
+    _call("harp_fp8_gemm_grouped", lib.harp_fp8_gemm_grouped, index, stream,
+          (W.ref, a.data_ptr(), a_scale.data_ptr(), a_rows, r, offsets.data_ptr(),
+           y.data_ptr(), _FLOATS[y.dtype], M))
 
 
 def harp_last_hip_error() -> int:
