@@ -614,7 +614,7 @@ struct TileCost {
   int bn, bm, bf16_ns, f32_ns;   // 0: not built
 };
 constexpr TileCost kTiles[] = {
-    {256, 256, 1800, 0}, {256, 128, 970, 0},  {128, 128, 610, 0}, {128, 128, 0, 1020},
+    {256, 256, 1800, 0}, {256, 128, 950, 0},  {128, 128, 610, 0}, {128, 128, 0, 1020},
     {128, 128, 0, 920},  {128, 64, 390, 690}, {64, 64, 280, 0},   {64, 32, 180, 245},
     {64, 16, 143, 165},  {32, 16, 105, 110},
 };
@@ -651,7 +651,7 @@ hipError_t launch_by_size(const Fp8Args& p, hipStream_t stream) {
       if constexpr (kBf16) return launch_tile<256, 256, 128, 64, 1, 2, YT>(p, live, stream);
       [[fallthrough]];
     case 1:
-      if constexpr (kBf16) return launch_tile<256, 128, 64, 64, 1, 3, YT>(p, live, stream);
+      if constexpr (kBf16) return launch_tile<256, 128, 128, 64, 1, 3, YT>(p, live, stream);
       [[fallthrough]];
     case 2:
       if constexpr (kBf16) return launch_tile<128, 128, 64, 64, 1, 4, YT>(p, live, stream);
