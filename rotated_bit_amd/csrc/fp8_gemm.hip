@@ -614,8 +614,8 @@ template <int BN, int BM, int WN, int WM, int KG, int STAGES, typename YT>
 hipError_t launch_tile(const Fp8Args& p, int live, hipStream_t stream) {
   const int n_tiles = (p.N + BN - 1) / BN;
   // sum_e ceil(c_e / BM) <= (M + live (BM - 1)) / BM.  With the tile picked
-  // below the threads stay under the 2^32 a launch may have (1.7e9 at most,
-  // for 40000 rows of 1024 experts with 262144 outputs).
+  // below the threads stay under the 2^32 a launch may have (3.1e9 at most,
+  // for 8192 rows of 1024 experts with 262144 outputs).
   const int m_tiles = static_cast<int>((p.M + static_cast<int64_t>(live) * (BM - 1)) / BM);
   fp8_tile_kernel<BN, BM, WN, WM, KG, STAGES, YT>
       <<<dim3(n_tiles * m_tiles), KG * BN / WN * (BM / WM) * kWave, 0, stream>>>(p, n_tiles,
@@ -623,74 +623,73 @@ hipError_t launch_tile(const Fp8Args& p, int live, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// The tiles, largest first, and what a run of 128 inputs costs a round of
-// 256 tiles (one per CU), in ns, measured from the second such round of 64
-// runs.  The estimate rounds x cost picks the tile: large ones do the most
-// work per time (256 x 256 bf16: 36 outputs per ns and CU, 128 x 64: 21,
-// 64 x 16: 7), small ones leave no CU idle where there are few outputs.
+// The tiles, largest first, and what a run of 128 inputs costs in ns,
+// measured over 64 runs: `one` per round of 256 tiles (one per CU), `two`,
+// where two workgroups fit a CU, per round of 512.  The estimate rounds x
+// cost picks the tile: large ones do the most work per time (bf16, outputs
+// per ns and CU: 256 x 256 36, 128 x 64 23, 32 x 16 7), small ones leave no
+// CU idle where there are few outputs, and two workgroups on a CU hide each
+// other's waits for memory.
 struct TileCost {
-  int bn, bm, bf16_ns, f32_ns;   // 0: not built
+  int bn, bm, one, two;   // two: 0 where one workgroup fills a CU
 };
-constexpr TileCost kTiles[] = {
-    {256, 256, 1800, 0}, {256, 128, 950, 0},  {128, 128, 610, 0}, {128, 128, 0, 1020},
-    {128, 128, 0, 920},  {128, 64, 390, 690}, {64, 64, 280, 0},   {64, 32, 180, 245},
-    {64, 16, 143, 165},  {32, 16, 105, 110},
+constexpr TileCost kBf16Tiles[] = {
+    {256, 256, 1800, 0}, {256, 128, 980, 0},   {128, 128, 610, 0},
+    {128, 64, 400, 720}, {64, 64, 250, 0},     {64, 32, 166, 282},
+    {32, 32, 117, 205},  {32, 16, 83, 150},    {16, 16, 50, 105},
 };
-constexpr int kSharedCu = 4;   // two workgroups share a CU: from two tiles per CU on
+constexpr TileCost kF32Tiles[] = {
+    {128, 128, 960, 0},  {128, 128, 1110, 1860}, {128, 64, 755, 1140}, {64, 64, 437, 660},
+    {64, 32, 339, 390},  {32, 32, 231, 250},     {32, 16, 88, 160},    {16, 16, 61, 120},
+};
 
-int pick_tile(const Fp8Args& p, int live, bool bf16) {
+template <int N>
+int pick_tile(const Fp8Args& p, int live, const TileCost (&tiles)[N]) {
   int best = 0;
   double least = 0.0;
   const double rows = static_cast<double>(p.M) / live;   // of an expert, on average
-  for (int i = 0; i < static_cast<int>(sizeof kTiles / sizeof kTiles[0]); ++i) {
-    const TileCost& c = kTiles[i];
-    const int ns = bf16 ? c.bf16_ns : c.f32_ns;
-    if (ns == 0) continue;
+  for (int i = 0; i < N; ++i) {
+    const TileCost& c = tiles[i];
     // an expert's last tile is half empty on average; dense rows are known
     double m_tiles = rows / c.bm + 0.5;
     if (m_tiles < 1.0) m_tiles = 1.0;
     m_tiles = p.offsets == nullptr ? (p.M + c.bm - 1) / c.bm : live * m_tiles;
-    const double rounds = ceil(m_tiles * ((p.N + c.bn - 1) / c.bn) / 256.0);
-    if (i == kSharedCu && rounds < 2.0) continue;
-    if (least == 0.0 || rounds * ns < least) {
-      least = rounds * ns;
+    const double count = m_tiles * ((p.N + c.bn - 1) / c.bn);
+    const double cost =
+        c.two != 0 && count > 256.0 ? ceil(count / 512.0) * c.two : ceil(count / 256.0) * c.one;
+    if (i == 0 || cost < least) {
+      least = cost;
       best = i;
     }
   }
   return best;
 }
 
-template <typename YT>
-hipError_t launch_by_size(const Fp8Args& p, hipStream_t stream) {
-  constexpr bool kBf16 = sizeof(YT) == 2;
-  const int live = p.offsets == nullptr ? 1 : (p.E < p.M ? p.E : p.M);   // experts with rows
-  switch (pick_tile(p, live, kBf16)) {
-    case 0:
-      if constexpr (kBf16) return launch_tile<256, 256, 128, 64, 1, 2, YT>(p, live, stream);
-      [[fallthrough]];
-    case 1:
-      if constexpr (kBf16) return launch_tile<256, 128, 128, 64, 1, 3, YT>(p, live, stream);
-      [[fallthrough]];
-    case 2:
-      if constexpr (kBf16) return launch_tile<128, 128, 64, 64, 1, 4, YT>(p, live, stream);
-      [[fallthrough]];
-    case 3:
-      if constexpr (!kBf16) return launch_tile<128, 128, 64, 64, 2, 2, YT>(p, live, stream);
-      [[fallthrough]];
-    case 4:
-      if constexpr (!kBf16) return launch_tile<128, 128, 64, 64, 1, 2, YT>(p, live, stream);
-      [[fallthrough]];
-    case 5:
-      return launch_tile<128, 64, 64, 32, 2, 3, YT>(p, live, stream);
-    case 6:
-      if constexpr (kBf16) return launch_tile<64, 64, 64, 32, 2, 4, YT>(p, live, stream);
-      [[fallthrough]];
-    case 7:
-      return launch_tile<64, 32, 64, 32, 4, 3, YT>(p, live, stream);
-    case 8:
-      return launch_tile<64, 16, 64, 16, 4, 3, YT>(p, live, stream);
-    default:
-      return launch_tile<32, 16, 32, 16, 8, 3, YT>(p, live, stream);
+hipError_t launch_by_size(const Fp8Args& p, int live, uint16_t*, hipStream_t stream) {
+  using T = uint16_t;
+  switch (pick_tile(p, live, kBf16Tiles)) {
+    case 0: return launch_tile<256, 256, 128, 64, 1, 2, T>(p, live, stream);
+    case 1: return launch_tile<256, 128, 128, 64, 1, 3, T>(p, live, stream);
+    case 2: return launch_tile<128, 128, 64, 64, 1, 4, T>(p, live, stream);
+    case 3: return launch_tile<128, 64, 64, 32, 1, 3, T>(p, live, stream);
+    case 4: return launch_tile<64, 64, 64, 32, 2, 4, T>(p, live, stream);
+    case 5: return launch_tile<64, 32, 64, 32, 2, 3, T>(p, live, stream);
+    case 6: return launch_tile<32, 32, 32, 32, 2, 4, T>(p, live, stream);
+    case 7: return launch_tile<32, 16, 32, 16, 4, 3, T>(p, live, stream);
+    default: return launch_tile<16, 16, 16, 16, 4, 4, T>(p, live, stream);
+  }
+}
+hipError_t launch_by_size(const Fp8Args& p, int live, float*, hipStream_t stream) {
+  using T = float;
+  switch (pick_tile(p, live, kF32Tiles)) {
+    case 0: return launch_tile<128, 128, 64, 64, 2, 2, T>(p, live, stream);
+    case 1: return launch_tile<128, 128, 64, 64, 1, 2, T>(p, live, stream);
+    case 2: return launch_tile<128, 64, 64, 32, 1, 3, T>(p, live, stream);
+    case 3: return launch_tile<64, 64, 64, 32, 2, 2, T>(p, live, stream);
+    case 4: return launch_tile<64, 32, 64, 32, 2, 3, T>(p, live, stream);
+    case 5: return launch_tile<32, 32, 32, 32, 2, 4, T>(p, live, stream);
+    case 6: return launch_tile<32, 16, 32, 16, 4, 3, T>(p, live, stream);
+    default: return launch_tile<16, 16, 16, 16, 4, 4, T>(p, live, stream);
   }
 }
 
@@ -701,8 +700,9 @@ hipError_t launch_fp8_gemm(const harp_fp8_weight& W, const uint8_t* a, const flo
                            int y_dt, int M, hipStream_t stream) {
   const Fp8Args p{W.w, W.scale, a,   a_scale,        rows,      offsets, y,
                   W.N, W.K,     fp8_runs(W.K), W.experts, M,       a_rows};
-  return y_dt == HARP_BF16 ? launch_by_size<uint16_t>(p, stream)
-                           : launch_by_size<float>(p, stream);
+  const int live = offsets == nullptr ? 1 : (p.E < M ? p.E : M);   // experts with rows, at most
+  return y_dt == HARP_BF16 ? launch_by_size(p, live, static_cast<uint16_t*>(nullptr), stream)
+                           : launch_by_size(p, live, static_cast<float*>(nullptr), stream);
 }
 
 }  // namespace harp

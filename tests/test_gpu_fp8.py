@@ -277,7 +277,9 @@ GROUPS = [
     ([2500, 2, 3000], 4100, 144, True), ([5, 0, 20], 4832, 400, True),
     ([0, 200, 5, 60, 20, 1, 20, 1, 20], 3330, 144, True),
     ([200, 5, 0, 100, 20, 1, 5, 0, 130], 3398, 272, True),
-    ([100, 5, 5, 0, 0, 100, 1, 0], 3734, 656, True),
+    ([100, 5, 5, 0, 0, 100, 1, 0], 3734, 656, True), ([0, 0, 5, 0, 1], 3274, 272, True),
+    ([1, 1, 1, 1, 5], 862, 400, True), ([1, 130, 5, 1, 20, 5], 4936, 144, True),
+    ([0, 0, 1, 1, 60, 5], 4535, 272, True),
     ([5, 60, 100, 5, 20, 60, 0, 300, 0, 0, 20], 4887, 144, False),
 ]
 
