@@ -4,11 +4,18 @@
 //     y[m][n] = sum_b sa[m][b] sw[n/128][b] P_b[m][n],
 //     P_b[m][n] = sum_{k in run b} a[m][k] w[n][k].
 //
-// For a bf16 y one v_mfma_f32_16x16x128_f8f6f4 forms P_b of 16 x 16 outputs (its 128
-// inputs are one run), so the scales enter once per matrix instruction as
-// four fused multiply-adds per lane.  The weights are the row operand and a
-// the column operand: lane l holds the four consecutive outputs
-// n0 + 4 (l / 16) + 0..3 of row m0 + l % 16, which share one factor sa sw.
+// For a bf16 y one v_mfma_f32_16x16x128_f8f6f4 forms P_b of 16 x 16 outputs
+// (its 128 inputs are one run), so the scales enter once per matrix
+// instruction as four fused multiply-adds per lane.  The weights are the row
+// operand and a the column operand: a lane holds four consecutive outputs of
+// one row of y, which share one factor sa sw.
+//
+// What bounds it (MI355X): with few rows the pass over the weights (16 x
+// 28672 x 8192: 43.5 us, 5.4 TB/s; 64 rows over 64 experts of 4096 x 4096:
+// 90 us, 5.1 TB/s; 1 x 4096 x 4096: 5.6 us, latency); with many rows LDS
+// traffic and power (4096 x 28672 x 8192: 806 us, 2.39 PFLOP/s, matrix pipe
+// 61 % busy; 711 us with zeros as inputs); in between how many tiles there
+// are for 256 CUs (512 x 4096 x 4096: 15.7 us, 1.09 PFLOP/s).
 #include <type_traits>
 
 #include "fp8_common.hpp"
@@ -198,7 +205,7 @@ __device__ __forceinline__ int w_key(int row) {
 }
 __device__ __forceinline__ int a_key(int row) { return (row >> 1) & 7; }
 
-// Descriptor of `bytes` bytes at address v (raw, no stride); wave-uniform.
+// Descriptor of `bytes` bytes at p (raw, no stride); wave-uniform.
 __device__ __forceinline__ u32x4 buffer_of(const void* p, uint32_t bytes) {
   const uint64_t v = reinterpret_cast<uint64_t>(p);
   return u32x4{static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(v))),
@@ -578,7 +585,8 @@ __global__ __launch_bounds__(KG* BN / WN * (BM / WM) * kWave) void fp8_tile_kern
   // Rows of y that keep the alignment of 16 bytes are written from the
   // registers.  Other rows go through LDS, each at the place in 16 bytes that
   // its first output has in memory, and from there in aligned pieces of 16
-  // bytes (2772 x 28631 x 576: 270 -> 57 us against one store per output).
+  // bytes (2772 x 28631 x 576: 132 us against 270 with a store per output,
+  // and 96 for 28632 outputs).
   constexpr int V = 16 / sizeof(YT), kPitch = BN + V, kPieces = kPitch / V;
   constexpr int kThreads = KG * G * kWave;
   static_assert(BM * kPitch * static_cast<int>(sizeof(YT)) <= kLds, "");

