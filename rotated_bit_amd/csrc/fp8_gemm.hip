@@ -155,22 +155,6 @@ __device__ __forceinline__ floatx4 mfma_run(i32x8 w, i32x8 a) {
     return d;
   }
 }
-// Two exact sums in turn: each of a sum's four instructions waits for the
-// one before it.
-__device__ __forceinline__ void mfma_run_pair(i32x8 w0, i32x8 a0, i32x8 w1, i32x8 a1,
-                                              floatx4& d0, floatx4& d1) {
-  d0 = d1 = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    d0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_bf16(w0[2 * i], w0[2 * i + 1]),
-                                                 codes_bf16(a0[2 * i], a0[2 * i + 1]), d0, 0, 0,
-                                                 0);
-    d1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_bf16(w1[2 * i], w1[2 * i + 1]),
-                                                 codes_bf16(a1[2 * i], a1[2 * i + 1]), d1, 0, 0,
-                                                 0);
-  }
-}
-
 // A buffer offset past the end of every descriptor used here: those are at
 // most kFp8MaxGather bytes (gathered rows) or 256 rows of K.
 constexpr uint32_t kOut = kFp8MaxGather;
@@ -486,6 +470,116 @@ __global__ __launch_bounds__(KG* BN / WN * (BM / WM) * kWave) void fp8_tile_kern
           for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(f[j], P[r], acc[i][j][r]);
         }
     });
+  } else if constexpr (kExact) {
+    // The order of the branch below (there it is explained), with the
+    // operands as bf16.  A sum is four matrix instructions; two sums, a pair,
+    // are formed in turn.  The vector ALU's work is laid between them, two
+    // conversions and one scaled addition to a matrix instruction (in turn
+    // with another wave's those take 23 cycles, 17 without any), so that no
+    // matrix instruction waits for an operand just converted: a fragment is
+    // read a pair before its conversion, which is at least a pair before its
+    // first use, and a sum is added a pair after it (200 x 11008 x 4096:
+    // 37.8 -> 33.4 us against conversions in front of the sums).
+    constexpr int kRest = TJ, kPairs = TI * TJ / 2, kHalf = TJ / 2;   // in pairs
+    constexpr int kPer = (kLoads + kPairs - 1) / kPairs;
+    static_assert(TJ % 2 == 0, "");
+    // pair p's two outputs: of the last two rows of weight tiles column by
+    // column, then of the other rows in order
+    auto row_of = [](int p, int u) { return p < kRest ? TI - 2 + u : (p - kRest) / kHalf; };
+    auto col_of = [](int p, int u) { return p < kRest ? p : (p - kRest) % kHalf * 2 + u; };
+    // the pair in which a fragment is converted: after the last use of the
+    // registers of the run before where there is room for that, and always
+    // before the fragment's first use
+    auto w_at = [](int i) { return i < TI - 2 ? kRest + i * kHalf - 1 : kPairs - TI + i; };
+    auto a_at = [](int j) { return j + 1 < kRest + j / 2 - 1 ? j + 1 : kRest + j / 2 - 1; };
+    i32x8 rw[TI], ra[TJ];                  // as read
+    bf16x8 xw[TI][4], xa[TJ][4], na[TJ][4];
+    floatx4 P[2][2];
+    float f_old[TJ], f[TJ];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      xw[TI - 2][q] = xw[TI - 1][q] = bf16x8{};
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) xa[j][q] = bf16x8{};
+    }
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) f[j] = 0.0f;
+    P[1][0] = P[1][1] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+    auto add = [&](int p, int u, const float (&by)[TJ]) {
+      floatx4& to = acc[row_of(p, u)][col_of(p, u)];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) to[r] = fmaf(by[col_of(p, u)], P[p % 2][u][r], to[r]);
+      asm volatile("" : "+v"(to));   // here, not at the end of the step
+    };
+    all_steps([&](int s, auto at) {
+      constexpr int stage = decltype(at)::value, next = (stage + kAhead) % STAGES;
+      arrive();
+      ready(s + kAhead);
+      const float swk = weight_scale(stage);
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        f_old[j] = f[j];
+        f[j] = row_scale(stage, j);
+      }
+#pragma unroll
+      for (int p = 0; p < kPairs; ++p) {
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+          if (w_at(i) - 1 == p) rw[i] = w_fragment(stage, i);
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+          if (a_at(j) - 1 == p) ra[j] = a_fragment(stage, j);
+        if (p == kRest) {
+#pragma unroll
+          for (int u = 0; u < TJ; ++u) f[u] *= swk;
+        }
+#pragma unroll
+        for (int u = p * kPer; u < (p + 1) * kPer && u < kLoads; ++u) load(u, next);
+        __builtin_amdgcn_sched_barrier(0);
+        P[p % 2][0] = P[p % 2][1] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            P[p % 2][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                xw[row_of(p, u)][q], xa[col_of(p, u)][q], P[p % 2][u], 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < TI; ++i)
+            if (w_at(i) == p) xw[i][q] = codes_bf16(rw[i][2 * q], rw[i][2 * q + 1]);
+#pragma unroll
+          for (int j = 0; j < TJ; ++j)
+            if (a_at(j) == p) na[j][q] = codes_bf16(ra[j][2 * q], ra[j][2 * q + 1]);
+          if (q >= 2) {
+            if (p == 0)
+              add(kPairs - 1, q - 2, f_old);
+            else
+              add(p - 1, q - 2, p - 1 < kRest ? f_old : f);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+          if (a_at(j) == p) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) xa[j][q] = na[j][q];
+          }
+      }
+    });
+    static_assert(kPairs % 2 == 0, "the last pair's sums are in P[1]");
+    add(kPairs - 1, 0, f);
+    add(kPairs - 1, 1, f);
+#pragma unroll
+    for (int p = 0; p < kRest; ++p) {
+      P[p % 2][0] = P[p % 2][1] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          P[p % 2][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              xw[row_of(p, u)][q], xa[col_of(p, u)][q], P[p % 2][u], 0, 0, 0);
+      add(p, 0, f);
+      add(p, 1, f);
+    }
   } else {
     // Step s: the products of the run before that are left (its last two
     // rows of weight tiles), under which the first operands of this run are
@@ -496,8 +590,7 @@ __global__ __launch_bounds__(KG* BN / WN * (BM / WM) * kWave) void fp8_tile_kern
     constexpr int kRows = 2, kRest = kRows * TJ;
     // the scaled addition of a product comes kLag products after its issue:
     // by then the matrix pipe has finished it and works on the later ones.
-    // Exact products are issued, and added, in pairs.
-    constexpr int kLag = kExact ? 2 : 3;
+    constexpr int kLag = 3;
     constexpr int kPer = (kLoads + kProducts - 1) / kProducts;
     i32x8 fa[TJ], fw[4];       // row i of weight tiles in fw[i % 4]
     float f_old[TJ], f[TJ];
@@ -534,12 +627,7 @@ __global__ __launch_bounds__(KG* BN / WN * (BM / WM) * kWave) void fp8_tile_kern
         const int i = row_of(n), j = col_of(n);
         if (n < 2) fw[n] = w_fragment(stage, n);
         if (n >= kRest && j == 0) fw[(i + 2) % 4] = w_fragment(stage, i + 2);
-        if constexpr (!kExact) {
-          P[n % 4] = mfma_run<false>(fw[i % 4], fa[j]);
-        } else if (n % 2 == 0) {
-          mfma_run_pair(fw[i % 4], fa[j], fw[row_of(n + 1) % 4], fa[col_of(n + 1)], P[n % 4],
-                        P[n % 4 + 1]);
-        }
+        P[n % 4] = mfma_run<false>(fw[i % 4], fa[j]);
         if (n < kRest && n % kRows == kRows - 1) fa[j] = a_fragment(stage, j);
         if (n == kRest) {
 #pragma unroll
@@ -559,7 +647,7 @@ __global__ __launch_bounds__(KG* BN / WN * (BM / WM) * kWave) void fp8_tile_kern
 #pragma unroll
     for (int n = 0; n < kRest; ++n) {
       const int i = row_of(n), j = col_of(n);
-      const floatx4 D = mfma_run<kExact>(fw[i % 4], fa[j]);
+      const floatx4 D = mfma_run<false>(fw[i % 4], fa[j]);
 #pragma unroll
       for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(f[j], D[r], acc[i][j][r]);
     }
