@@ -739,28 +739,40 @@ hipError_t launch_tile(const Fp8Args& p, int live, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// The tiles, largest first, and what a run of 128 inputs costs in ns,
-// measured over 64 runs: `one` per round of 256 tiles (one per CU), `two`,
-// where two workgroups fit a CU, per round of 512.  The estimate rounds x
-// cost picks the tile: large ones do the most work per time (bf16, outputs
-// per ns and CU: 256 x 256 36, 128 x 64 23, 32 x 16 7), small ones leave no
-// CU idle where there are few outputs, and two workgroups on a CU hide each
-// other's waits for memory.
+// The tiles, largest first, with what they take in us, from least squares
+// over 1200 products (16 .. 65536 rows and outputs, K 1024 .. 8192; residual
+// 6 %): up to 256 tiles, one per CU, `lone` and `lone_run` for each run of 128
+// inputs; beyond, `round` and `round_run` for each round of `per` tiles (512
+// where two workgroups fit a CU and hide each other's waits); and on top
+// kF32Output or kBf16Output for each 2^20 outputs and run, the matrix pipe's
+// power and the shared bandwidth.  The estimate picks the tile: large ones do
+// the most work per time, small ones leave no CU idle where there are few
+// outputs, and what a round takes before and behind its runs counts where K
+// is small.  Over 78 products of drawn sizes the picked tile is within 1 %
+// (float32 y) and 2 % (bf16) of the fastest on average, 22 % at worst; a
+// cost per run alone left 3.5 %, 44 % at worst.
 struct TileCost {
-  int bn, bm, one, two;   // two: 0 where one workgroup fills a CU
+  int bn, bm, per;
+  float lone, lone_run, round, round_run;
 };
+constexpr float kBf16Output = 0.064f, kF32Output = 0.081f;
 constexpr TileCost kBf16Tiles[] = {
-    {256, 256, 1800, 0}, {256, 128, 980, 0},   {128, 128, 610, 0},
-    {128, 64, 400, 720}, {64, 64, 250, 0},     {64, 32, 166, 282},
-    {32, 32, 117, 205},  {32, 16, 83, 150},    {16, 16, 50, 105},
+    {256, 256, 256, 6.3f, 0.861f, 6.3f, 0.861f}, {256, 128, 256, 4.8f, 0.525f, 4.8f, 0.525f},
+    {128, 128, 256, 3.3f, 0.362f, 3.3f, 0.362f}, {128, 128, 512, 2.0f, 0.588f, 3.2f, 0.606f},
+    {128, 64, 512, 2.5f, 0.265f, 2.2f, 0.428f},  {64, 64, 256, 2.8f, 0.171f, 2.8f, 0.171f},
+    {64, 32, 512, 2.9f, 0.146f, 2.9f, 0.225f},   {32, 32, 512, 2.3f, 0.094f, 2.4f, 0.162f},
+    {32, 16, 512, 2.3f, 0.060f, 2.3f, 0.105f},   {16, 16, 512, 2.1f, 0.044f, 2.3f, 0.077f},
 };
 constexpr TileCost kF32Tiles[] = {
-    {128, 128, 960, 0},  {128, 128, 1110, 1860}, {128, 64, 755, 1140}, {64, 64, 437, 660},
-    {64, 32, 339, 390},  {32, 32, 231, 250},     {32, 16, 88, 160},    {16, 16, 61, 120},
+    {128, 128, 256, 5.1f, 0.572f, 5.1f, 0.572f}, {128, 128, 512, 4.9f, 0.707f, 3.7f, 1.004f},
+    {128, 64, 512, 3.7f, 0.501f, 3.0f, 0.690f},  {64, 64, 512, 2.3f, 0.340f, 2.8f, 0.384f},
+    {64, 32, 512, 2.8f, 0.281f, 3.4f, 0.247f},   {64, 32, 256, 3.5f, 0.126f, 3.5f, 0.126f},
+    {32, 32, 512, 2.0f, 0.137f, 2.3f, 0.168f},   {32, 16, 512, 2.3f, 0.073f, 2.3f, 0.114f},
+    {16, 16, 512, 2.2f, 0.055f, 2.3f, 0.082f},
 };
 
 template <int N>
-int pick_tile(const Fp8Args& p, int live, const TileCost (&tiles)[N]) {
+int pick_tile(const Fp8Args& p, int live, const TileCost (&tiles)[N], float output) {
   int best = 0;
   double least = 0.0;
   const double rows = static_cast<double>(p.M) / live;   // of an expert, on average
@@ -771,8 +783,11 @@ int pick_tile(const Fp8Args& p, int live, const TileCost (&tiles)[N]) {
     if (m_tiles < 1.0) m_tiles = 1.0;
     m_tiles = p.offsets == nullptr ? (p.M + c.bm - 1) / c.bm : live * m_tiles;
     const double count = m_tiles * ((p.N + c.bn - 1) / c.bn);
-    const double cost =
-        c.two != 0 && count > 256.0 ? ceil(count / 512.0) * c.two : ceil(count / 256.0) * c.one;
+    double cost = output * p.KB * count * (c.bn * c.bm / 1048576.0);
+    if (count <= 256.0)
+      cost += c.lone + p.KB * c.lone_run;
+    else
+      cost += ceil(count / c.per) * (c.round + p.KB * c.round_run);
     if (i == 0 || cost < least) {
       least = cost;
       best = i;
@@ -783,28 +798,30 @@ int pick_tile(const Fp8Args& p, int live, const TileCost (&tiles)[N]) {
 
 hipError_t launch_by_size(const Fp8Args& p, int live, uint16_t*, hipStream_t stream) {
   using T = uint16_t;
-  switch (pick_tile(p, live, kBf16Tiles)) {
+  switch (pick_tile(p, live, kBf16Tiles, kBf16Output)) {
     case 0: return launch_tile<256, 256, 128, 64, 1, 2, T>(p, live, stream);
     case 1: return launch_tile<256, 128, 128, 64, 1, 3, T>(p, live, stream);
     case 2: return launch_tile<128, 128, 64, 64, 1, 4, T>(p, live, stream);
-    case 3: return launch_tile<128, 64, 64, 32, 1, 3, T>(p, live, stream);
-    case 4: return launch_tile<64, 64, 64, 32, 2, 4, T>(p, live, stream);
-    case 5: return launch_tile<64, 32, 64, 32, 2, 3, T>(p, live, stream);
-    case 6: return launch_tile<32, 32, 32, 32, 2, 4, T>(p, live, stream);
-    case 7: return launch_tile<32, 16, 32, 16, 4, 3, T>(p, live, stream);
+    case 3: return launch_tile<128, 128, 64, 64, 1, 2, T>(p, live, stream);
+    case 4: return launch_tile<128, 64, 64, 32, 1, 3, T>(p, live, stream);
+    case 5: return launch_tile<64, 64, 64, 32, 2, 4, T>(p, live, stream);
+    case 6: return launch_tile<64, 32, 64, 32, 2, 3, T>(p, live, stream);
+    case 7: return launch_tile<32, 32, 32, 32, 2, 4, T>(p, live, stream);
+    case 8: return launch_tile<32, 16, 32, 16, 4, 3, T>(p, live, stream);
     default: return launch_tile<16, 16, 16, 16, 4, 4, T>(p, live, stream);
   }
 }
 hipError_t launch_by_size(const Fp8Args& p, int live, float*, hipStream_t stream) {
   using T = float;
-  switch (pick_tile(p, live, kF32Tiles)) {
+  switch (pick_tile(p, live, kF32Tiles, kF32Output)) {
     case 0: return launch_tile<128, 128, 64, 64, 2, 2, T>(p, live, stream);
     case 1: return launch_tile<128, 128, 64, 64, 1, 2, T>(p, live, stream);
     case 2: return launch_tile<128, 64, 64, 32, 1, 3, T>(p, live, stream);
     case 3: return launch_tile<64, 64, 64, 32, 2, 2, T>(p, live, stream);
     case 4: return launch_tile<64, 32, 64, 32, 2, 3, T>(p, live, stream);
-    case 5: return launch_tile<32, 32, 32, 32, 2, 4, T>(p, live, stream);
-    case 6: return launch_tile<32, 16, 32, 16, 4, 3, T>(p, live, stream);
+    case 5: return launch_tile<64, 32, 64, 32, 4, 3, T>(p, live, stream);
+    case 6: return launch_tile<32, 32, 32, 32, 4, 2, T>(p, live, stream);
+    case 7: return launch_tile<32, 16, 32, 16, 4, 3, T>(p, live, stream);
     default: return launch_tile<16, 16, 16, 16, 4, 4, T>(p, live, stream);
   }
 }

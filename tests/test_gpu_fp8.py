@@ -310,6 +310,27 @@ def test_grouped(sizes, N, K, gather, dt):
     check_product(y[2:2 + live], ref, mag, K, dt)
 
 
+# Many runs of K, with a ragged last one: large tiles and split runs.
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", [
+    (2361, 1686, 2480), (1239, 1561, 2064), (714, 1399, 1264), (260, 980, 4400),
+    (1237, 1642, 2208), (2675, 891, 2208), (1306, 391, 1456), (670, 885, 1616),
+    (591, 425, 3600), (456, 578, 4368), (33, 1100, 8336)])
+def test_product_long(M, N, K, dt):
+    test_product(M, N, K, dt)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("sizes,N,K,gather", [
+    ([1500, 3, 1098], 1737, 2576, True),
+    ([400, 0, 300, 1, 500, 200, 366, 250, 250], 824, 2736, False),
+    ([300, 0, 0, 1, 200, 100, 257, 100, 100], 787, 1136, True),
+    ([1000, 320, 1000], 849, 2384, False), ([5, 60, 0, 100, 100, 1, 39, 0, 0], 1746, 400, True),
+    ([3, 0, 60], 1864, 480, False), ([470, 0, 300], 352, 4272, True)])
+def test_grouped_long(sizes, N, K, gather, dt):
+    test_grouped(sizes, N, K, gather, dt)
+
+
 @pytest.mark.parametrize("sizes", [[2, 3], [40, 90], [300, 500]])
 def test_grouped_rows_out_of_range_are_zero(sizes):
     rng = np.random.default_rng(8)
