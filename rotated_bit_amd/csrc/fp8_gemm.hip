@@ -176,18 +176,25 @@ __device__ __forceinline__ i32x8 join(u32x4 lo, u32x4 hi) {
 // past its descriptor's end writes zeros, which covers rows past the tile
 // and, with the offset pushed out of range, the inputs from K on.
 //
-// LDS rows hold their eight 16-byte chunks at chunk ^ key(row), so that the
-// 16 lanes that read 16 bytes each at a time, from 16 rows, hit all 64 banks
-// (two rows' chunk slots): rows of one parity have eight keys.  With S = up
-// to 4 matrix tiles of 16 outputs side by side in a wave, tile i takes the
-// LDS rows 4 S (r / 4) + 4 i + r % 4 (r = 0..15), so that a lane's results
-// over the S tiles are 4 S consecutive outputs and a row of y is written in
-// long pieces (whole 128-byte lines for S = 4).
+// With S = up to 4 matrix tiles of 16 outputs side by side in a wave, tile i
+// takes the LDS rows 4 S (r / 4) + 4 i + r % 4 (r = 0..15), so that a lane's
+// results over the S tiles are 4 S consecutive outputs and a row of y is
+// written in long pieces (whole 128-byte lines for S = 4).
+// LDS rows hold their eight 16-byte chunks at chunk ^ key(row).  A 16-byte
+// read serves 16 lanes at a time, each from a row r of its own: lanes 0-3,
+// 12-15 and 20-27, then 4-11, 16-19 and 28-31, and so on from 32 (measured).
+// Both hold every r, but r = 4..11 in the other half of 32 lanes than the
+// rest, which reads the chunk two places off: bit 1 of its place is r2 ^ r3
+// (bits of r) or the complement.  With key = r1 + 6 r3 the place after the
+// exclusive or has r1, r2 and r3 as its bits, up to constants, and r0 tells
+// between two rows' slots, so the 16 reads fall on all 64 banks (4096 x
+// 28672 x 8192: LDS busy 27 % of the time, against 51 % with the conflicts of
+// key = r / 2; 820 -> 812 us, power binds there).
 template <int S>
 __device__ __forceinline__ int w_key(int row) {
-  return ((row >> 1) & 1) | ((row >> (S == 4 ? 3 : S == 2 ? 2 : 1)) & 6);
+  return ((row >> 1) & 1) | (6 * ((row >> (S == 4 ? 5 : S == 2 ? 4 : 3)) & 1));
 }
-__device__ __forceinline__ int a_key(int row) { return (row >> 1) & 7; }
+__device__ __forceinline__ int a_key(int row) { return w_key<1>(row); }
 
 // Descriptor of `bytes` bytes at p (raw, no stride); wave-uniform.
 __device__ __forceinline__ u32x4 buffer_of(const void* p, uint32_t bytes) {
