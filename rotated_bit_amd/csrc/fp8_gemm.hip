@@ -39,9 +39,12 @@ struct Fp8Args {
 };
 
 // The tile a workgroup works on: outputs from nt BN on of the rows
-// [row0, row0 + count) of expert e.
+// [row0, row0 + count) of expert e.  near_rows row tiles next to each other in
+// the order work on its weights, it is the row_at-th of them; and near_outs
+// output tiles on its rows, out_at.
 struct Tile {
   int e, nt, row0, count;
+  int row_at, near_rows, out_at, near_outs;
 };
 
 // Order of the tiles: expert after expert; an expert's k row tiles x n_tiles
@@ -113,8 +116,12 @@ __device__ __forceinline__ bool find_tile(const Fp8Args& p, int id, int n_tiles,
   const int width = min(w, n_tiles - panel * w), in = r - panel * w * k;
   const int block = in / (kBlock * width), rest = in - block * kBlock * width;
   const int height = min(kBlock, k - block * kBlock);
-  t.nt = panel * w + rest / height;
-  t.row0 += BM * (block * kBlock + rest % height);
+  t.row_at = rest % height;
+  t.near_rows = height;
+  t.out_at = rest / height;
+  t.near_outs = width;
+  t.nt = panel * w + t.out_at;
+  t.row0 += BM * (block * kBlock + t.row_at);
   t.count = min(BM, end - t.row0);
   return true;
 }
@@ -270,12 +277,25 @@ __global__ __launch_bounds__(KG* BN / WN * (BM / WM) * kWave) void fp8_tile_kern
   constexpr int kSLoads = (kRowSlots + 1 + G - 1) / G, kSlots = kSLoads * G;
   constexpr int kAhead = STAGES - 1;            // runs in flight
   constexpr int kLoads = kWLoads + kALoads + kSLoads;   // of a wave per run
-  static_assert((kAhead - 1) * kLoads < 64, "the counter of loads in flight");
+  // The 256 x 256 tile has room for two runs in LDS only, so a run's loads
+  // have at most one step to arrive, less than a line from beyond L2 takes
+  // at times.  Its waves therefore also ask for one dword of each line three
+  // runs further on, which brings the line into L2; each workgroup asks for
+  // its share of the lines it has in common with its neighbours.  These two
+  // loads are a step's last and may stay in flight over the barrier (4096 x
+  // 28672 x 8192: 812 -> 793 us, 721 -> 631 with zeros as inputs; 512 rows
+  // 130 -> 122).  Tiles with three stages or two workgroups a CU lose by it
+  // (256 x 128 grouped 426 -> 479 us, 128 x 128 1024 -> 1112).
+  constexpr bool kTouch = BN + BM > 384;
+  constexpr int kTouches = kTouch ? 2 : 0, kTouchAhead = 2;
+  static_assert(kAhead * kTouches + (kAhead - 1) * kLoads < 64, "the counter of loads in flight");
+  static_assert(!kTouch || (KG == 1 && TI >= 4 && !kExact), "touch() stands there only");
   // one array: the stages' w rows, their a rows, their scales, so that a
   // stage is an immediate offset of the reads
   constexpr int kWRun = BN * kFp8Run, kARun = kARows * kFp8Run, kSRun = kSlots * kWave * 4;
   constexpr int kABase = STAGES * KG * kWRun, kSBase = kABase + STAGES * KG * kARun;
-  constexpr int kLds = kSBase + STAGES * KG * kSRun;
+  constexpr int kTBase = kSBase + STAGES * KG * kSRun;   // 256 bytes per wave, never read
+  constexpr int kLds = kTBase + (kTouch ? G * kWave * 4 : 0);
   static_assert(kLds <= 160 * 1024 && (KG - 1) * G * TI * TJ * 1024 <= kLds, "");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
   Tile t;
@@ -379,11 +399,31 @@ __global__ __launch_bounds__(KG* BN / WN * (BM / WM) * kWave) void fp8_tile_kern
       move(ds[u], KG * 4);
     }
   };
+  // lane 8 r + i touches row r of the wave's load i, if that row is in its share
+  uint32_t touch_w = kOut, touch_a = kOut, past = 0;
+  if constexpr (kTouch) {
+    static_assert(kWLoads <= 8 && kALoads <= 8, "");
+    const int i = lane & 7, row = lr + i * kRowsPerLoad;
+    if (i < kWLoads && row % t.near_rows == t.row_at) touch_w = row * K + kTouchAhead * kFp8Run;
+    uint32_t at = kOut;
+#pragma unroll
+    for (int u = 0; u < kALoads; ++u)
+      if (i == u && aoff[u] < kOut) at = aoff[u] - ac(u);
+    if (at < kOut && row % t.near_outs == t.out_at) touch_a = at + kTouchAhead * kFp8Run;
+  }
+  // after the loads of a run, whose descriptors then stand at the next one
+  auto touch = [&]() {
+    if constexpr (kTouch) {
+      load_lds4(dw, touch_w | past, lds_base + kTBase + gw * (kWave * 4));
+      load_lds4(da, touch_a | past, lds_base + kTBase + gw * (kWave * 4));
+    }
+  };
   // before the loads of step s's run
   auto ready = [&](int s) {
     const int kb = s * KG + group;
     if (tail != 0 && kb == KB - 1) cut();
     keep = kb + KG < KB ? ~0u : 0u;
+    if constexpr (kTouch) past = kb + 1 + kTouchAhead < KB ? 0u : kOut;
   };
 
   const int wn = (gw % (BN / WN)) * WN, wm = (gw / (BN / WN)) * WM;
@@ -418,11 +458,12 @@ __global__ __launch_bounds__(KG* BN / WN * (BM / WM) * kWave) void fp8_tile_kern
   auto weight_scale = [&](int stage) {
     return sc[stage * (KG * kSRun / 4) + kRowSlots * kWave + wn / kFp8Run];
   };
-  // this wave's loads of the step's run have arrived (later ones may still be
-  // in flight) and its reads of the step before are done; after the barrier
+  // this wave's loads of the step's run have arrived (later ones, and the
+  // touches behind each run's, may still be in flight) and its reads of the step before are done; after the barrier
   // that holds for every wave.  A group of one wave loads for itself.
   auto arrive = [&]() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((kAhead - 1) * kLoads) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((kAhead - 1) * kLoads + kAhead * kTouches)
+                 : "memory");
     if constexpr (G > 1) __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
@@ -435,6 +476,7 @@ __global__ __launch_bounds__(KG* BN / WN * (BM / WM) * kWave) void fp8_tile_kern
     ready(s);
 #pragma unroll
     for (int n = 0; n < kLoads; ++n) load(n, s);
+    touch();
   }
   const int steps = (KB + KG - 1) / KG;
   auto all_steps = [&](auto step) {
@@ -462,6 +504,7 @@ __global__ __launch_bounds__(KG* BN / WN * (BM / WM) * kWave) void fp8_tile_kern
       ready(s + kAhead);
 #pragma unroll
       for (int n = 0; n < kLoads; ++n) load(n, (decltype(at)::value + kAhead) % STAGES);
+      touch();
     });
   } else if constexpr (TI < 4) {
     all_steps([&](int s, auto at) {
@@ -659,6 +702,7 @@ __global__ __launch_bounds__(KG* BN / WN * (BM / WM) * kWave) void fp8_tile_kern
         if (n >= kLag) add(n - kLag);
         __builtin_amdgcn_sched_barrier(0);
       }
+      touch();
 #pragma unroll
       for (int n = kProducts - kLag; n < kProducts; ++n) add(n);
     });

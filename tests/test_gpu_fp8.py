@@ -331,6 +331,19 @@ def test_grouped_long(sizes, N, K, gather, dt):
     test_grouped(sizes, N, K, gather, dt)
 
 
+# The largest tiles over enough runs to ask for lines ahead, the last tiles of
+# a row or an expert with waves that have no row or no output.
+@pytest.mark.parametrize("M,N,K", [(3900, 4240, 912), (4000, 4001, 1168)])
+def test_product_large(M, N, K):
+    test_product(M, N, K, "bf16")
+
+
+@pytest.mark.parametrize("sizes,N,K,gather", [([2000, 3, 1900, 90], 5000, 1040, True),
+                                              ([1, 2600, 2399], 3400, 912, False)])
+def test_grouped_large(sizes, N, K, gather):
+    test_grouped(sizes, N, K, gather, "bf16")
+
+
 @pytest.mark.parametrize("sizes", [[2, 3], [40, 90], [300, 500]])
 def test_grouped_rows_out_of_range_are_zero(sizes):
     rng = np.random.default_rng(8)
