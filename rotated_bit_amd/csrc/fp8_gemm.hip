@@ -11,10 +11,10 @@
 // one row of y, which share one factor sa sw.
 //
 // What bounds it (MI355X): with few rows the pass over the weights (16 x
-// 28672 x 8192: 43.5 us, 5.4 TB/s; 64 rows over 64 experts of 4096 x 4096:
-// 90 us, 5.1 TB/s; 1 x 4096 x 4096: 5.6 us, latency); with many rows LDS
-// traffic and power (4096 x 28672 x 8192: 806 us, 2.39 PFLOP/s, matrix pipe
-// 61 % busy; 711 us with zeros as inputs); in between how many tiles there
+// 28672 x 8192: 44.8 us, 5.3 TB/s; 64 rows over 64 experts of 4096 x 4096:
+// 84 us, 5.4 TB/s; 1 x 4096 x 4096: 5.4 us, latency); with many rows power
+// (4096 x 28672 x 8192: 793 to 827 us, 2.33 PFLOP/s and more, matrix pipe
+// 68 % busy; 631 us with zeros as inputs); in between how many tiles there
 // are for 256 CUs (512 x 4096 x 4096: 15.7 us, 1.09 PFLOP/s).
 #include <type_traits>
 
