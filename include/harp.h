@@ -518,9 +518,9 @@ typedef struct harp_fp8_weight {
  * products the codes of harp_rmsnorm_fp8):
  *     h = x + r,   r' = h rounded to x_dt,   y = h / sqrt(mean(h^2) + eps) * w.
  * The norm is taken of h in float32, before r' is rounded; the sum of
- * squares is float32 (a row in which it overflows, from about 1e19, comes out
- * as zeros; a NaN or infinity in h makes its row NaN, or NaN in its place and
- * zero elsewhere).
+ * squares is float32, of a row scaled by a power of two where the squares
+ * would leave float32's range.  A NaN in h makes its row NaN, an infinity
+ * comes out as NaN in its place and zero elsewhere.
  *   x             [M][D] of x_dt;  weight [D] of w_dt
  *   residual      [M][D] of x_dt, or NULL (h = x)
  *   residual_out  [M][D] of x_dt, or NULL (r' is not stored; must be NULL

@@ -5,7 +5,8 @@
 //
 // One workgroup per row for the norm: the row is read once and stays in
 // registers (float32) over the sum of squares, so a row moves x, r in and
-// r', y out and nothing else.  A thread holds chunks of 8 consecutive
+// r', y out and nothing else.  A row whose squares leave float32's range is
+// scaled in its registers and summed again (scaled_mean).  A thread holds chunks of 8 consecutive
 // values; the 16 lanes of a DPP row hold one run of 128, whose maximum is
 // four lane rotations.  Both are bound by memory (MI355X: norm of 8192 x
 // 8192 bf16 to codes 82.7 us, 5.7 TB/s; activation of 2000 x 28672 55.4 us,
@@ -40,10 +41,59 @@ __device__ __forceinline__ void store_chunk(T* row, int d, int D, const float (&
   }
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
+// Sum / maximum of v over the workgroup, the same bits in every thread.  All
+// threads call; part is free again after the next barrier.
+__device__ __forceinline__ float block_sum(float v, float* part) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += shfl_xor(v, o);
+  if ((threadIdx.x & (kWave - 1)) == 0) part[threadIdx.x / kWave] = v;
+  __syncthreads();
+  v = 0.0f;
+  for (int i = 0; i < static_cast<int>(blockDim.x) / kWave; ++i) v += part[i];
   return v;
+}
+__device__ __forceinline__ float block_max(float v, float* part) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, shfl_xor(v, o));
+  if ((threadIdx.x & (kWave - 1)) == 0) part[threadIdx.x / kWave] = v;
+  __syncthreads();
+  v = 0.0f;
+  for (int i = 0; i < static_cast<int>(blockDim.x) / kWave; ++i) v = fmaxf(v, part[i]);
+  return v;
+}
+
+// mean(h^2) + eps below which the squares may have lost bits as subnormal
+// numbers: those are off by 2^-150 each, so the mean by as much, 2^-50 of it.
+constexpr float kLeastMean = 0x1p-100f;
+constexpr int kScaledExponent = 50;   // 2^100 per square, 32768 of them
+
+// The mean of a row whose squares leave float32's range: the row in h is
+// taken times the power of two that brings the largest of |h| and sqrt(eps)
+// just below 2^50, and its mean and eps are that power's square larger, which
+// h / sqrt(mean + eps) does not see.  Rows of zeros without eps, of NaN and of
+// infinities keep `mean`.  The whole workgroup calls, or none of it.
+template <int C>
+__device__ __forceinline__ float scaled_mean(float (&h)[C][8], float mean, float eps, int D,
+                                             float* part) {
+  float m = sqrtf(eps);
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(h[c][i]));
+  __syncthreads();
+  m = block_max(m, part);
+  if (m == 0.0f || m == INFINITY) return mean;
+  const int by = kScaledExponent - __builtin_amdgcn_frexp_expf(m);
+  float ss = 0.0f;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      h[c][i] = ldexpf(h[c][i], by);
+      ss = fmaf(h[c][i], h[c][i], ss);
+    }
+  __syncthreads();
+  return block_sum(ss, part) / static_cast<float>(D) + ldexpf(eps, 2 * by);
 }
 
 // Codes and scale of the chunk's run; all 16 lanes of the run's row call.
@@ -91,12 +141,9 @@ __global__ __launch_bounds__(kNormThreads) void rmsnorm_kernel(
 #pragma unroll
     for (int i = 0; i < 8; ++i) ss = fmaf(h[c][i], h[c][i], ss);
   }
-  ss = wave_sum(ss);
-  if (lane == 0) part[t / kWave] = ss;
-  __syncthreads();
-  ss = 0.0f;
-  for (int i = 0; i < static_cast<int>(blockDim.x) / kWave; ++i) ss += part[i];
-  const float r = 1.0f / sqrtf(ss / static_cast<float>(D) + eps);
+  float mean = block_sum(ss, part) / static_cast<float>(D) + eps;
+  if (mean < kLeastMean || mean == INFINITY) mean = scaled_mean<C>(h, mean, eps, D, part);
+  const float r = 1.0f / sqrtf(mean);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int d = 8 * (c * blockDim.x + t);

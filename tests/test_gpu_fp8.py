@@ -170,6 +170,61 @@ def test_norm_special_rows():
     check_codes(q[4:5], s[4:5], F.rmsnorm(f64(x[4:5]), None, f64(w), 1e-6)[1])
 
 
+# Rows whose squares leave float32's range, either way.  h is scaled by a power
+# of two there (exact), so the bounds above hold; eps next to h decides how
+# much of the mean it is.  y below 2^-126 is a subnormal number: its two
+# products are off by half a subnormal step each, 2^-150, the first times w.
+FAR_EPS = [0.0, 1e-44, 1e-38, 1e-30, 1e-6, 1e30, 3e38]
+FAR_MAG = [1e-44, 1e-41, 1e-36, 1e-30, 1e-24, 1e-18, 1e-12, 1.0, 1e16, 1e18, 1e19, 1e20, 1e30,
+           5e37]
+
+
+def far_rows(rng, D, dt):
+    """Rows of each magnitude, then rows in which one value stands out."""
+    a = np.clip(rng.standard_normal((2 * len(FAR_MAG), D)), -3, 3)
+    a[:, 0] = 2.0                                        # a row is never all zeros
+    mag = np.array(FAR_MAG)[:, None]
+    if dt == "bf16":                                     # whose least value is 2^-133
+        mag = np.maximum(mag, 1e-39)
+    a[:len(FAR_MAG)] *= mag
+    a[len(FAR_MAG):, D // 2:] *= mag
+    return rounded(a, dt)
+
+
+@pytest.mark.parametrize("y_dt", ["f32", "bf16"])
+@pytest.mark.parametrize("x_dt", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [1, 16, 272, 5121, 9008, 16400, 32768])
+def test_norm_far_from_one(D, x_dt, y_dt):
+    rng = np.random.default_rng(D + 40)
+    x, x64 = far_rows(rng, D, x_dt)
+    w, w64 = rounded(np.clip(1 + 0.2 * rng.standard_normal(D), 0.25, 2), "f32")
+    y = torch.empty(x.shape, dtype=DT[y_dt], device="cuda")
+    r = torch.empty_like(x)
+    for eps in FAR_EPS:
+        eps64 = float(np.float32(eps))
+        lib().harp_rmsnorm(x, w, y, eps=eps, residual=torch.zeros_like(x), residual_out=r)
+        assert torch.equal(r, x)                         # stored as it is, not scaled
+        ref = F.rmsnorm(x64, None, w64, eps64)[1]
+        tol = (VALUE_TOL * (1 + HALF[y_dt]) + HALF[y_dt]) * np.abs(ref) + 3 * 2.0 ** -150
+        if y_dt == "bf16":
+            tol += 2.0 ** -134                           # half a subnormal bf16 step
+        off = np.abs(f64(y) - ref)
+        assert np.all(off <= tol), (eps, np.argwhere(~(off <= tol))[0])
+
+
+@pytest.mark.parametrize("x_dt", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [16, 272, 9008, 32768])
+def test_norm_fp8_far_from_one(D, x_dt):
+    rng = np.random.default_rng(D + 41)
+    x, x64 = far_rows(rng, D, x_dt)
+    x, x64 = x[:len(FAR_MAG)], x64[:len(FAR_MAG)]
+    w, w64 = rounded(np.clip(1 + 0.2 * rng.standard_normal(D), 0.25, 2), "f32")
+    q = torch.empty(x.shape, dtype=E4, device="cuda")
+    s = torch.empty((x.shape[0], F.runs(D)), device="cuda")
+    lib().harp_rmsnorm_fp8(x, w, q, s, eps=0.0)          # y is about 1 in every row
+    check_codes(q, s, F.rmsnorm(x64, None, w64, 0.0)[1])
+
+
 @pytest.mark.parametrize("x_dt", ["f32", "bf16"])
 @pytest.mark.parametrize("M,D", [(1, 16), (3, 144), (16, 11008), (130, 2064), (5, 128),
                                  (1, 262144), (700, 272)])
