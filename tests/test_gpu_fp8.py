@@ -226,6 +226,37 @@ def test_norm_fp8_far_from_one(D, x_dt):
 
 
 @pytest.mark.parametrize("x_dt", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [272, 9008])
+def test_norm_infinity_and_nan_in_a_row(D, x_dt):
+    # an infinity: NaN in its place, zero elsewhere; a NaN: the whole row; a
+    # sum of x and residual beyond float32 is an infinity
+    x = torch.ones((4, D), dtype=DT[x_dt], device="cuda")
+    x[0, 7] = float("inf")
+    x[1, 7] = float("-inf")
+    x[1, 200] = float("nan")
+    x[2, 7] = 3e38
+    r = torch.zeros_like(x)
+    r[2, 7] = 3e38
+    w = torch.ones(D, device="cuda")
+    other = torch.arange(D, device="cuda") != 7
+    for eps in (0.0, 1e-6):
+        for y_dt in ("f32", "bf16"):
+            y = torch.empty(x.shape, dtype=DT[y_dt], device="cuda")
+            lib().harp_rmsnorm(x, w, y, eps=eps, residual=r)
+            for row in (0, 2):
+                assert torch.isnan(y[row, 7]) and torch.all(y[row][other] == 0)
+            assert torch.isnan(y[1]).all()
+            assert torch.all((y[3].float() - 1).abs() <= 2.0 ** -8)
+        q = torch.empty(x.shape, dtype=E4, device="cuda")
+        s = torch.empty((4, F.runs(D)), device="cuda")
+        lib().harp_rmsnorm_fp8(x, w, q, s, eps=eps, residual=r)
+        for row in (0, 2):
+            assert torch.isnan(q[row, 7].float()) and torch.all(q[row].float()[other] == 0)
+            assert torch.all(s[row] == 2.0 ** -126)
+        assert torch.isnan(q[1].float()).all() and torch.all(s[1] == 2.0 ** -126)
+
+
+@pytest.mark.parametrize("x_dt", ["f32", "bf16"])
 @pytest.mark.parametrize("M,D", [(1, 16), (3, 144), (16, 11008), (130, 2064), (5, 128),
                                  (1, 262144), (700, 272)])
 def test_silu_mul(M, D, x_dt):
