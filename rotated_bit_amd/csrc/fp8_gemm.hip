@@ -19,6 +19,7 @@
 #include <type_traits>
 
 #include "fp8_common.hpp"
+#include "fp8_pick.hpp"
 #include "launch.hpp"
 #include "validate.hpp"
 
@@ -786,105 +787,48 @@ __global__ __launch_bounds__(KG* BN / WN * (BM / WM) * kWave) void fp8_tile_kern
   }
 }
 
-// ---- choice of the tile -----------------------------------------------------------
+// ---- launch -----------------------------------------------------------------------
 
-template <int BN, int BM, int WN, int WM, int KG, int STAGES, typename YT>
+// The tile of entry I of the table for YT (fp8_pick.hpp).
+template <int I, int BN, int BM, int WN, int WM, int KG, int STAGES, typename YT>
 hipError_t launch_tile(const Fp8Args& p, int live, hipStream_t stream) {
-  const int n_tiles = (p.N + BN - 1) / BN;
-  // sum_e ceil(c_e / BM) <= (M + live (BM - 1)) / BM.  With the tile picked
-  // below the threads stay under the 2^32 a launch may have (3.1e9 at most,
-  // for 8192 rows of 1024 experts with 262144 outputs).
-  const int m_tiles = static_cast<int>((p.M + static_cast<int64_t>(live) * (BM - 1)) / BM);
+  constexpr int kThreads = KG * BN / WN * (BM / WM) * kWave;
+  constexpr Fp8Tile tile = sizeof(YT) == 2 ? kBf16Tiles[I] : kF32Tiles[I];
+  static_assert(tile.bn == BN && tile.bm == BM && tile.threads == kThreads, "");
+  const int n_tiles = static_cast<int>(fp8_n_tiles(tile, p.N));
+  const int m_tiles = static_cast<int>(fp8_m_tiles(tile, p.M, live));
   fp8_tile_kernel<BN, BM, WN, WM, KG, STAGES, YT>
-      <<<dim3(n_tiles * m_tiles), KG * BN / WN * (BM / WM) * kWave, 0, stream>>>(p, n_tiles,
-                                                                                 m_tiles);
+      <<<dim3(n_tiles * m_tiles), kThreads, 0, stream>>>(p, n_tiles, m_tiles);
   return hipGetLastError();
-}
-
-// The tiles, largest first, with what they take in us, from least squares
-// over 1200 products (16 .. 65536 rows and outputs, K 1024 .. 8192; residual
-// 6 %): up to 256 tiles, one per CU, `lone` and `lone_run` for each run of 128
-// inputs; beyond, `round` and `round_run` for each round of `per` tiles (512
-// where two workgroups fit a CU and hide each other's waits); and on top
-// kF32Output or kBf16Output for each 2^20 outputs and run, the matrix pipe's
-// power and the shared bandwidth.  The estimate picks the tile: large ones do
-// the most work per time, small ones leave no CU idle where there are few
-// outputs, and what a round takes before and behind its runs counts where K
-// is small.  Over 78 products of drawn sizes the picked tile is within 1 %
-// (float32 y) and 2 % (bf16) of the fastest on average, 22 % at worst; a
-// cost per run alone left 3.5 %, 44 % at worst.
-struct TileCost {
-  int bn, bm, per;
-  float lone, lone_run, round, round_run;
-};
-constexpr float kBf16Output = 0.064f, kF32Output = 0.081f;
-constexpr TileCost kBf16Tiles[] = {
-    {256, 256, 256, 6.3f, 0.861f, 6.3f, 0.861f}, {256, 128, 256, 4.8f, 0.525f, 4.8f, 0.525f},
-    {128, 128, 256, 3.3f, 0.362f, 3.3f, 0.362f}, {128, 128, 512, 2.0f, 0.588f, 3.2f, 0.606f},
-    {128, 64, 512, 2.5f, 0.265f, 2.2f, 0.428f},  {64, 64, 256, 2.8f, 0.171f, 2.8f, 0.171f},
-    {64, 32, 512, 2.9f, 0.146f, 2.9f, 0.225f},   {32, 32, 512, 2.3f, 0.094f, 2.4f, 0.162f},
-    {32, 16, 512, 2.3f, 0.060f, 2.3f, 0.105f},   {16, 16, 512, 2.1f, 0.044f, 2.3f, 0.077f},
-};
-constexpr TileCost kF32Tiles[] = {
-    {128, 128, 256, 5.1f, 0.572f, 5.1f, 0.572f}, {128, 128, 512, 4.9f, 0.707f, 3.7f, 1.004f},
-    {128, 64, 512, 3.7f, 0.501f, 3.0f, 0.690f},  {64, 64, 512, 2.3f, 0.340f, 2.8f, 0.384f},
-    {64, 32, 512, 2.8f, 0.281f, 3.4f, 0.247f},   {64, 32, 256, 3.5f, 0.126f, 3.5f, 0.126f},
-    {32, 32, 512, 2.0f, 0.137f, 2.3f, 0.168f},   {32, 16, 512, 2.3f, 0.073f, 2.3f, 0.114f},
-    {16, 16, 512, 2.2f, 0.055f, 2.3f, 0.082f},
-};
-
-template <int N>
-int pick_tile(const Fp8Args& p, int live, const TileCost (&tiles)[N], float output) {
-  int best = 0;
-  double least = 0.0;
-  const double rows = static_cast<double>(p.M) / live;   // of an expert, on average
-  for (int i = 0; i < N; ++i) {
-    const TileCost& c = tiles[i];
-    // an expert's last tile is half empty on average; dense rows are known
-    double m_tiles = rows / c.bm + 0.5;
-    if (m_tiles < 1.0) m_tiles = 1.0;
-    m_tiles = p.offsets == nullptr ? (p.M + c.bm - 1) / c.bm : live * m_tiles;
-    const double count = m_tiles * ((p.N + c.bn - 1) / c.bn);
-    double cost = output * p.KB * count * (c.bn * c.bm / 1048576.0);
-    if (count <= 256.0)
-      cost += c.lone + p.KB * c.lone_run;
-    else
-      cost += ceil(count / c.per) * (c.round + p.KB * c.round_run);
-    if (i == 0 || cost < least) {
-      least = cost;
-      best = i;
-    }
-  }
-  return best;
 }
 
 hipError_t launch_by_size(const Fp8Args& p, int live, uint16_t*, hipStream_t stream) {
   using T = uint16_t;
-  switch (pick_tile(p, live, kBf16Tiles, kBf16Output)) {
-    case 0: return launch_tile<256, 256, 128, 64, 1, 2, T>(p, live, stream);
-    case 1: return launch_tile<256, 128, 128, 64, 1, 3, T>(p, live, stream);
-    case 2: return launch_tile<128, 128, 64, 64, 1, 4, T>(p, live, stream);
-    case 3: return launch_tile<128, 128, 64, 64, 1, 2, T>(p, live, stream);
-    case 4: return launch_tile<128, 64, 64, 32, 1, 3, T>(p, live, stream);
-    case 5: return launch_tile<64, 64, 64, 32, 2, 4, T>(p, live, stream);
-    case 6: return launch_tile<64, 32, 64, 32, 2, 3, T>(p, live, stream);
-    case 7: return launch_tile<32, 32, 32, 32, 2, 4, T>(p, live, stream);
-    case 8: return launch_tile<32, 16, 32, 16, 4, 3, T>(p, live, stream);
-    default: return launch_tile<16, 16, 16, 16, 4, 4, T>(p, live, stream);
+  switch (fp8_pick(kBf16Tiles, kBf16Output, p.M, p.N, p.K, live, p.offsets != nullptr)) {
+    case 0: return launch_tile<0, 256, 256, 128, 64, 1, 2, T>(p, live, stream);
+    case 1: return launch_tile<1, 256, 128, 128, 64, 1, 3, T>(p, live, stream);
+    case 2: return launch_tile<2, 128, 128, 64, 64, 1, 4, T>(p, live, stream);
+    case 3: return launch_tile<3, 128, 128, 64, 64, 1, 2, T>(p, live, stream);
+    case 4: return launch_tile<4, 128, 64, 64, 32, 1, 3, T>(p, live, stream);
+    case 5: return launch_tile<5, 64, 64, 64, 32, 2, 4, T>(p, live, stream);
+    case 6: return launch_tile<6, 64, 32, 64, 32, 2, 3, T>(p, live, stream);
+    case 7: return launch_tile<7, 32, 32, 32, 32, 2, 4, T>(p, live, stream);
+    case 8: return launch_tile<8, 32, 16, 32, 16, 4, 3, T>(p, live, stream);
+    default: return launch_tile<9, 16, 16, 16, 16, 4, 4, T>(p, live, stream);
   }
 }
 hipError_t launch_by_size(const Fp8Args& p, int live, float*, hipStream_t stream) {
   using T = float;
-  switch (pick_tile(p, live, kF32Tiles, kF32Output)) {
-    case 0: return launch_tile<128, 128, 64, 64, 2, 2, T>(p, live, stream);
-    case 1: return launch_tile<128, 128, 64, 64, 1, 2, T>(p, live, stream);
-    case 2: return launch_tile<128, 64, 64, 32, 1, 3, T>(p, live, stream);
-    case 3: return launch_tile<64, 64, 64, 32, 2, 2, T>(p, live, stream);
-    case 4: return launch_tile<64, 32, 64, 32, 2, 3, T>(p, live, stream);
-    case 5: return launch_tile<64, 32, 64, 32, 4, 3, T>(p, live, stream);
-    case 6: return launch_tile<32, 32, 32, 32, 4, 2, T>(p, live, stream);
-    case 7: return launch_tile<32, 16, 32, 16, 4, 3, T>(p, live, stream);
-    default: return launch_tile<16, 16, 16, 16, 4, 4, T>(p, live, stream);
+  switch (fp8_pick(kF32Tiles, kF32Output, p.M, p.N, p.K, live, p.offsets != nullptr)) {
+    case 0: return launch_tile<0, 128, 128, 64, 64, 2, 2, T>(p, live, stream);
+    case 1: return launch_tile<1, 128, 128, 64, 64, 1, 2, T>(p, live, stream);
+    case 2: return launch_tile<2, 128, 64, 64, 32, 1, 3, T>(p, live, stream);
+    case 3: return launch_tile<3, 64, 64, 64, 32, 2, 2, T>(p, live, stream);
+    case 4: return launch_tile<4, 64, 32, 64, 32, 2, 3, T>(p, live, stream);
+    case 5: return launch_tile<5, 64, 32, 64, 32, 4, 3, T>(p, live, stream);
+    case 6: return launch_tile<6, 32, 32, 32, 32, 4, 2, T>(p, live, stream);
+    case 7: return launch_tile<7, 32, 16, 32, 16, 4, 3, T>(p, live, stream);
+    default: return launch_tile<8, 16, 16, 16, 16, 4, 4, T>(p, live, stream);
   }
 }
 
@@ -895,7 +839,7 @@ hipError_t launch_fp8_gemm(const harp_fp8_weight& W, const uint8_t* a, const flo
                            int y_dt, int M, hipStream_t stream) {
   const Fp8Args p{W.w, W.scale, a,   a_scale,        rows,      offsets, y,
                   W.N, W.K,     fp8_runs(W.K), W.experts, M,       a_rows};
-  const int live = offsets == nullptr ? 1 : (p.E < M ? p.E : M);   // experts with rows, at most
+  const int live = fp8_live(M, p.E, offsets != nullptr);
   return y_dt == HARP_BF16 ? launch_by_size(p, live, static_cast<uint16_t*>(nullptr), stream)
                            : launch_by_size(p, live, static_cast<float*>(nullptr), stream);
 }
