@@ -42,6 +42,21 @@ SOURCE_FLAGS = {"fp8_gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 CXX_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall"]
 
 
+# Sources with loads into LDS in inline assembly, whose wait states hazards.py
+# looks over in the object file.
+LDS_LOAD_SOURCES = ["fp8_gemm.hip"]
+
+
+def _hazards():
+    """hazards.py, by path (the package itself loads the library)."""
+    import importlib.util
+    spec = importlib.util.spec_from_file_location("_harp_hazards",
+                                                  os.path.join(HERE, "hazards.py"))
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
 def hipcc() -> str:
     for cand in (os.environ.get("HIPCC"), "/opt/rocm/bin/hipcc", shutil.which("hipcc")):
         if cand and os.path.exists(cand):
@@ -89,6 +104,9 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
             print(" ".join(c))
             if o.strip():
                 print(o)
+    llvm = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "llvm", "bin")
+    for src in LDS_LOAD_SOURCES:
+        _hazards().check_object(os.path.join(BUILD, src + ".o"), llvm=llvm, arch=ARCH)
     tmp = LIB + ".tmp"
     link = [cc, "-shared", "-fPIC", f"--offload-arch={ARCH}", "-mcode-object-version=5"]
     tl = torch_lib_dir()

@@ -215,17 +215,23 @@ __device__ __forceinline__ u32x4 buffer_of(const void* p, uint32_t bytes) {
 }
 // 16 (4) bytes per lane from descriptor r at off to LDS address
 // lds + 16 (4) lane.  The s_nop is the wait state between the write of m0 and
-// the load; r is scalar arithmetic's, except before the first load of all
-// (settle()).
+// the load.  A load also needs five behind a vector instruction's write of a
+// scalar that it reads, which the compiler does not see to for inline
+// assembly: settle() stands in front of the first load of all, whose r comes
+// from v_readfirstlane; later r are scalar arithmetic's, but where the compiler
+// spills scalars, v_readlane brings them back, and the build looks through the
+// machine code and refuses a load that follows too closely (build.py).  Five
+// wait states in each block would do as well, at up to 2 % of the large
+// products and 8 % of 64 x 4096 x 4096 (6.5 -> 7.0 us).
 __device__ __forceinline__ void load_lds16(u32x4 r, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds),
                "v"(off), "s"(r)
-               : "memory");
+               : "memory", "m0");
 }
 __device__ __forceinline__ void load_lds4(u32x4 r, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds),
                "v"(off), "s"(r)
-               : "memory");
+               : "memory", "m0");
 }
 // The wait states between a vector write of a scalar and a load that uses it.
 __device__ __forceinline__ void settle() { asm volatile("s_nop 7" ::: "memory"); }
