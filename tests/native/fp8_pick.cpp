@@ -3,6 +3,7 @@
 //
 //   fp8_pick            lines "bf16|f32 M N K experts grouped" from standard
 //                       input -> "index bn bm threads workgroups"
+//   fp8_pick tables     the number of entries of each table
 //   fp8_pick launches   the most threads of any launch over sizes up to the
 //                       largest, with the tables' costs and with costs that
 //                       make the smallest tiles look free
@@ -55,6 +56,11 @@ int main(int argc, char** argv) {
                 static_cast<long long>(most_if_small_were_free(kBf16Tiles)),
                 static_cast<long long>(most(kF32Tiles, kF32Output)),
                 static_cast<long long>(most_if_small_were_free(kF32Tiles)));
+    return 0;
+  }
+  if (argc > 1 && std::strcmp(argv[1], "tables") == 0) {
+    std::printf("bf16 %zu\nf32 %zu\n", sizeof(kBf16Tiles) / sizeof(Fp8Tile),
+                sizeof(kF32Tiles) / sizeof(Fp8Tile));
     return 0;
   }
   char dt[8];

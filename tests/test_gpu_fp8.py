@@ -417,8 +417,8 @@ def test_grouped_long(sizes, N, K, gather, dt):
     test_grouped(sizes, N, K, gather, dt)
 
 
-# The largest tiles over enough runs to ask for lines ahead, the last tiles of
-# a row or an expert with waves that have no row or no output.
+# Large products, with waves that have no row or no output in the last tiles of
+# a row or an expert (test_gpu_fp8_tiles.py: each tile by name).
 @pytest.mark.parametrize("M,N,K", [(3900, 4240, 912), (4000, 4001, 1168)])
 def test_product_large(M, N, K):
     test_product(M, N, K, "bf16")
