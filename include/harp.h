@@ -552,8 +552,9 @@ harp_status harp_silu_mul_fp8(const void *gate_up, harp_dtype x_dt, uint8_t *q, 
 /*
  * y[m][n] = sum_b a_scale[m][b] W->scale[n / 128][b] sum_{k in run b} a[m][k] w[n][k]
  * on the matrix cores: each run of 128 inputs is summed there, its two
- * scales are multiplied in float32 (their product must not overflow), and
- * the scaled runs are added in float32.  Any M.  For a bf16 y the run's sum
+ * scales are multiplied in float32 (their product must not overflow; below
+ * 2^-126 it has fewer bits, off by up to 2^-150), and the scaled runs are
+ * added in float32.  For a bf16 y the run's sum
  * is the FP8 matrix instruction's, which keeps the products of each eight
  * consecutive inputs to 2^-13 of the largest of them; for a float32 y it is
  * a float32 sum of the exact products (the codes taken to bf16, half the
@@ -568,9 +569,9 @@ harp_status harp_fp8_gemm(const harp_fp8_weight *W, const uint8_t *a, const floa
  * The same product for M rows that are sorted by expert, with as many rows
  * for each as a router chose: for offsets[e] <= i < offsets[e + 1]
  *     y[i] = W_e a[rows[i]].
- *   a        [a_rows][W->K] codes;  a_scale [a_rows][ceil(K/128)] float32
- *            (with rows, a_rows K at most 2^32 - 256 bytes:
- *            HARP_ERR_UNSUPPORTED beyond)
+ *   a        [a_rows][W->K] codes;  a_scale [a_rows][ceil(K/128)] float32;
+ *            1 <= a_rows <= HARP_MAX_M, 0 only with M == 0 (with rows,
+ *            a_rows K at most 2^32 - 256 bytes: HARP_ERR_UNSUPPORTED beyond)
  *   rows     [M] int32, or NULL for rows[i] = i (then a_rows >= M).  The same
  *            row may occur any number of times.  An entry outside
  *            [0, a_rows) makes its output row zero.

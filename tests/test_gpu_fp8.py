@@ -713,3 +713,26 @@ def test_norm_feeds_both_linears(M):
     H.harp_fp8_gemm(W8, q, s, y8)
     check_product(y8, *F.product(q.view(torch.uint8).cpu().numpy(), f64(s), wq[0], ws[0]), K,
                   "f32")
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("M", [3, 300])
+def test_product_of_scales_below_the_normal_range(M, dt):
+    # sa sw is float32: below 2^-126 it is off by half a subnormal step, 2^-150,
+    # which enters y times the run's sum; all else as ever
+    rng = np.random.default_rng(M + 70)
+    N, K = 272, 400
+    W, wq, ws = weight(rng, N, K)
+    a, sa, aq, as_ = rows_of(rng, M, K)
+    for down in (100, 109, 114, 117):
+        s = np.ldexp(as_, -down).astype(np.float32)      # exact: scales from 2^-8 on
+        assert np.array_equal(np.ldexp(s.astype(np.float64), down), as_)
+        y = torch.empty((M, N), dtype=DT[dt], device="cuda")
+        lib().harp_fp8_gemm(W, a, torch.from_numpy(s).cuda(), y)
+        ref, mag = F.product(aq, s, wq[0], ws[0])
+        ones = np.ones_like
+        plain = F.product(aq, ones(s), wq[0], ones(ws[0]))[1]      # sums of |a w|
+        drop = 7 * 2.0 ** -13 if dt == "bf16" else 0.0
+        tol = ((259 + F.runs(K) + 32) * U + drop) * mag + HALF[dt] * np.abs(ref) * (1 + drop)
+        tol = tol * (1 + HALF[dt]) + 2.0 ** -150 * plain * (1 + HALF[dt] + drop) + 2.0 ** -134
+        assert np.all(np.abs(f64(y) - ref) <= tol)
