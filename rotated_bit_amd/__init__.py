@@ -1,8 +1,9 @@
 """rotated_bit_amd: MI355X (gfx950) HIP implementation of the HARP rotated
 low-bit linear, y = U deq(Wq) V^T x, behind the C ABI of include/harp.h.
 
-The Python surface is the ctypes binding in _lib (argument marshalling only);
-importing this package fails if libharp.so has not been built.
+The Python surface is the ctypes binding in _lib (argument marshalling, and
+checks of the 8-bit operators' tensors); importing this package fails if
+libharp.so has not been built.
 """
 from ._lib import (  # noqa: F401
     HARP_BF16, HARP_F32, FP8Weight, HarpError, MixedRotation, harp_fp8_gemm,

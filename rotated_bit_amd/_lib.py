@@ -1,7 +1,7 @@
 """ctypes binding of libharp.so (include/harp.h).
 
-Argument marshalling only: every step of the path runs in the library's HIP
-kernels.  torch is used for device memory and the current stream.  The
+Argument marshalling, and for the 8-bit operators checks of the tensors: every
+step of the path runs in the library's HIP kernels.  torch is used for device memory and the current stream.  The
 functions carry the C names; tensors are passed by ``data_ptr()`` on
 ``torch.cuda.current_stream()`` unless a stream handle is given.
 

@@ -13,7 +13,7 @@
 // What bounds it (MI355X): with few rows the pass over the weights (16 x
 // 28672 x 8192: 44.8 us, 5.3 TB/s; 64 rows over 64 experts of 4096 x 4096:
 // 84 us, 5.4 TB/s; 1 x 4096 x 4096: 5.4 us, latency); with many rows power
-// (4096 x 28672 x 8192: 793 to 827 us, 2.33 PFLOP/s and more, matrix pipe
+// (4096 x 28672 x 8192: 784 to 827 us, 2.33 PFLOP/s and more, matrix pipe
 // 68 % busy; 631 us with zeros as inputs); in between how many tiles there
 // are for 256 CUs (512 x 4096 x 4096: 15.7 us, 1.09 PFLOP/s).
 #include <type_traits>
@@ -290,8 +290,8 @@ __global__ __launch_bounds__(KG* BN / WN * (BM / WM) * kWave) void fp8_tile_kern
   // runs further on, which brings the line into L2; each workgroup asks for
   // its share of the lines it has in common with its neighbours.  These two
   // loads are a step's last and may stay in flight over the barrier (4096 x
-  // 28672 x 8192: 812 -> 793 us, 721 -> 631 with zeros as inputs; 512 rows
-  // 130 -> 122).  Tiles with three stages or two workgroups a CU lose by it
+  // 28672 x 8192: 812 -> 793 us on one card, 847 -> 826 on another, there 721 ->
+  // 631 with zeros as inputs; 512 rows 134 -> 126).  Tiles with three stages or two workgroups a CU lose by it
   // (256 x 128 grouped 426 -> 479 us, 128 x 128 1024 -> 1112).
   constexpr bool kTouch = BN + BM > 384;
   constexpr int kTouches = kTouch ? 2 : 0, kTouchAhead = 2;
@@ -466,8 +466,9 @@ __global__ __launch_bounds__(KG* BN / WN * (BM / WM) * kWave) void fp8_tile_kern
     return sc[stage * (KG * kSRun / 4) + kRowSlots * kWave + wn / kFp8Run];
   };
   // this wave's loads of the step's run have arrived (later ones, and the
-  // touches behind each run's, may still be in flight) and its reads of the step before are done; after the barrier
-  // that holds for every wave.  A group of one wave loads for itself.
+  // touches behind each run's, may still be in flight) and its reads of the
+  // step before are done; after the barrier that holds for every wave.  A group
+  // of one wave loads for itself.
   auto arrive = [&]() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((kAhead - 1) * kLoads + kAhead * kTouches)
                  : "memory");

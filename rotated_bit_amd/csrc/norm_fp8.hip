@@ -11,7 +11,8 @@
 // four lane rotations.  Both are bound by memory (MI355X: norm of 8192 x
 // 8192 bf16 to codes 82.7 us, 5.7 TB/s; activation of 2000 x 28672 55.4 us,
 // 5.2 TB/s) down to a few hundred rows (333 x 5120 float32: 6.8 us, 3.5
-// TB/s, one round of loads, sum and stores); one row of 4096 takes 2.5 us.
+// TB/s: three trips to memory one behind the other, x, the residual, and
+// the weight behind the sum, then the stores); one row of 4096 takes 2.5 us.
 #include "fp8_common.hpp"
 #include "launch.hpp"
 
