@@ -541,7 +541,8 @@ harp_status harp_rmsnorm_fp8(const void *x, harp_dtype x_dt, const void *residua
 
 /*
  * The gated activation between an MLP's (or an expert's) two products, as
- * codes: v = g / (1 + exp(-g)) * u in float32.
+ * codes: v = g / (1 + exp(-g)) * u in float32 (for a finite g below -88.73
+ * exp(-g) overflows and v is zero; g = -infinity gives NaN).
  *   gate_up     [M][2 D] of x_dt, a row's D gates g first, then its D values u
  *   q, q_scale  codes of v as above;  D a multiple of 16, 16 <= D <=
  *               HARP_MAX_DIM

@@ -286,6 +286,31 @@ def test_silu_mul_special_values():
     assert torch.isfinite(v[384:]).all() and torch.isfinite(s[0, 3])
 
 
+@pytest.mark.parametrize("x_dt", ["f32", "bf16"])
+def test_silu_mul_gates_past_the_exponential(x_dt):
+    # one gate per run, u = 1: the run's scale is that gate's |v| / 448
+    gates = [-80.0, -88.0, -89.0, -1000.0, -3e38, float("-inf"), 88.0, 1000.0, 3e38]
+    D = 128 * len(gates)
+    x = torch.zeros((1, 2 * D), dtype=DT[x_dt], device="cuda")
+    x[0, D:] = 1.0
+    x[0, 0:D:128] = torch.tensor(gates, dtype=DT[x_dt], device="cuda")
+    g = f64(x[0, 0:D:128])
+    q = torch.empty((1, D), dtype=E4, device="cuda")
+    s = torch.empty((1, len(gates)), device="cuda")
+    lib().harp_silu_mul_fp8(x, q, s)
+    code, s = q.float()[0, ::128], f64(s)[0]
+    # at -80 and -88 the exponential is off by |g| u / ln 2 + 4 u, all else by
+    # 10 u: under 2^-16; v / 448 lies below the least scale at -88
+    v = g[:2] * np.exp(g[:2]) / (1 + np.exp(g[:2]))
+    assert code[0] == -448 and abs(s[0] * 448 / -v[0] - 1) <= 2.0 ** -16
+    ends = [F.decode(F.encode(v[1] * 2.0 ** 126 * (1 + d))) for d in (-2.0 ** -16, 2.0 ** -16)]
+    assert min(ends) <= float(code[1]) <= max(ends)
+    assert torch.isnan(code[5]) and torch.all(code[2:5] == 0)
+    assert np.all(s[1:6] == 2.0 ** -126)
+    assert torch.all(code[6:] == 448) and np.all(np.abs(s[6:] * 448 / g[6:] - 1) <= 2.0 ** -17)
+    assert torch.all(q.float()[0].reshape(-1, 128)[:, 1:] == 0)
+
+
 # ---- product ------------------------------------------------------------------
 
 def weight(rng, N, K, experts=None):
